@@ -10,7 +10,10 @@ raises: there is no fallback path.
 Entry points (same names as the C ABI):
   dspark_markov_draft, dspark_confidence, dspark_survival, dspark_schedule,
   dspark_schedule_ex, dspark_verify_pack, dspark_verify_greedy, dspark_accept_prob,
-  dspark_markov_draft_workspace, dspark_schedule_workspace, dspark_w2_store_from_rv.
+  dspark_markov_draft_workspace, dspark_schedule_workspace, dspark_w2_store_from_rv;
+verification over a paged key/value cache (paged.py): dspark_page_map,
+  dspark_page_trim, dspark_kv_store, dspark_kv_commit, dspark_tree_attention,
+  dspark_tree_attention_workspace, dspark_tree_pack, dspark_verify_tree.
 """
 from __future__ import annotations
 
@@ -28,7 +31,11 @@ __all__ = [
     "dspark_schedule_ex", "dspark_verify_pack", "dspark_verify_greedy", "dspark_accept_prob",
     "dspark_markov_draft_workspace", "dspark_schedule_workspace", "dspark_w2_store_from_rv",
     "ScheduleInfo", "SCHED_GLOBAL", "SCHED_EARLY_STOP", "SCHED_CAPACITY",
+    "dspark_page_map", "dspark_page_trim", "dspark_kv_store", "dspark_kv_commit",
+    "dspark_tree_attention", "dspark_tree_attention_workspace", "dspark_tree_pack",
+    "dspark_verify_tree",
 ]
+_PAGED = frozenset(__all__[-8:])
 
 GREEDY = 0
 SAMPLE = 1
@@ -39,6 +46,16 @@ SCHED_EARLY_STOP = 1
 SCHED_CAPACITY = 2
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
+
+
+def __getattr__(name):
+    # paged.py needs PyTorch at import; the package itself does not
+    if name in _PAGED:
+        from . import paged
+        for n in _PAGED:
+            globals()[n] = getattr(paged, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def lib_path() -> str:
@@ -141,6 +158,23 @@ def lib() -> ctypes.CDLL:
     L.dspark_accept_prob.restype = i32
     L.dspark_w2_store_from_rv.argtypes = [vp, i32, i32, vp, vp]
     L.dspark_w2_store_from_rv.restype = i32
+    i64 = ctypes.c_int64
+    L.dspark_page_map.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.dspark_page_trim.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.dspark_kv_store.argtypes = [vp, vp, i64, i64, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                  vp, vp, vp, vp, vp]
+    L.dspark_kv_commit.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, i32, i32, i32,
+                                   i32, i32, i32, i32, vp, vp]
+    L.dspark_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32]
+    L.dspark_tree_attention_workspace.restype = sz
+    L.dspark_tree_attention.argtypes = [vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32,
+                                        i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, i64, vp,
+                                        vp, sz, vp]
+    L.dspark_tree_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    L.dspark_verify_tree.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    for f in (L.dspark_page_map, L.dspark_page_trim, L.dspark_kv_store, L.dspark_kv_commit,
+              L.dspark_tree_attention, L.dspark_tree_pack, L.dspark_verify_tree):
+        f.restype = i32
     _LIB = L
     return L
 

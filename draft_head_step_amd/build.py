@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libdspark.so")
 SOURCES = ["api.hip", "markov_step.hip", "markov_pick_greedy_row.hip", "markov_pick_greedy_col.hip",
            "markov_pick_sample_row.hip", "markov_pick_sample_col.hip", "markov_pick_bias_only.hip",
            "confidence.hip", "schedule.hip", "verify.hip", "noalloc.hip", "rnn_head.hip",
-           "layout.hip"]
+           "layout.hip", "api_paged.hip", "pages.hip", "kv_cache.hip", "tree_pack.hip",
+           "tree_attention.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -28,6 +28,14 @@ dspark_status check_launch(const char* what) {
   return DSPARK_OK;
 }
 
+void clear_error() { g_last_error[0] = 0; }
+
+dspark_status allow_lds(const void* kernel, int bytes, const char* what) {
+  if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return fail(DSPARK_EDEVICE, "%s: hipFuncSetAttribute failed", what);
+  return DSPARK_OK;
+}
+
 // Host-visible argument checks of the Markov-head draft (everything except the
 // workspace), shared by the entry points that launch it.
 dspark_status check_markov_args(const uint16_t* W1, const uint16_t* W2, const float* base,

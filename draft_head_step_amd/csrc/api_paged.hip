@@ -1,0 +1,245 @@
+// C ABI entry points of the verification over a paged cache: host-side argument
+// validation, then kernel launches (as in api.hip).
+#include <math.h>
+
+#include "dspark_internal.h"
+#include "paged.h"
+
+namespace dspark {
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool head_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
+
+dspark_status check_pages(const char* who, int page_size, int max_pages, int num_pages) {
+  if (max_pages <= 0 || num_pages <= 0)
+    return fail(DSPARK_EINVAL, "%s: max_pages and num_pages must be positive", who);
+  if (page_shift(page_size) < 0)
+    return fail(DSPARK_EINVAL, "%s: page_size must be a power of two in [16, 1024] (got %d)", who,
+                page_size);
+  return DSPARK_OK;
+}
+
+dspark_status check_cache_types(const char* who, int dtype, int cache_dtype, const float* k_scale,
+                                const float* v_scale) {
+  if (dtype != DSPARK_BF16 && dtype != DSPARK_FP16)
+    return fail(DSPARK_EINVAL, "%s: dtype must be DSPARK_BF16 or DSPARK_FP16 (got %d)", who, dtype);
+  if (cache_dtype != dtype && cache_dtype != DSPARK_E4M3)
+    return fail(DSPARK_EINVAL, "%s: the cache must hold dtype or DSPARK_E4M3 (got %d)", who,
+                cache_dtype);
+  const bool f8 = cache_dtype == DSPARK_E4M3;
+  if (f8 ? (!k_scale || !v_scale) : (k_scale || v_scale))
+    return fail(DSPARK_EINVAL, "%s: scales go with a DSPARK_E4M3 cache, and with no other", who);
+  return DSPARK_OK;
+}
+
+}  // namespace
+}  // namespace dspark
+
+using dspark::fail;
+
+extern "C" {
+
+dspark_status dspark_page_map(const int32_t* cur_len, const int32_t* cu_seqlens, int R,
+                              int max_tokens, int page_size, int max_pages, int num_pages,
+                              int32_t* block_table, const int32_t* ring,
+                              const dspark_page_pool* pool, dspark_page_pool* pool_out,
+                              int64_t* slots, int32_t* new_len, void* stream) {
+  dspark::clear_error();
+  if (!cur_len || !cu_seqlens || !block_table || !ring || !pool || !pool_out || !slots || !new_len)
+    return fail(DSPARK_EINVAL, "page_map: NULL required pointer");
+  if (R <= 0 || max_tokens <= 0) return fail(DSPARK_EINVAL, "page_map: sizes must be positive");
+  const dspark_status st = dspark::check_pages("page_map", page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  if (pool == pool_out || new_len == cur_len)
+    return fail(DSPARK_EINVAL, "page_map: pool_out and new_len need addresses of their own");
+  if (R > DSPARK_MAX_PAGE_REQUESTS)
+    return fail(DSPARK_EUNSUPPORTED, "page_map: more than %d requests", DSPARK_MAX_PAGE_REQUESTS);
+  return dspark::launch_page_map(cur_len, cu_seqlens, R, max_tokens, dspark::page_shift(page_size),
+                                 max_pages, num_pages, block_table, ring, pool, pool_out, slots,
+                                 new_len, reinterpret_cast<hipStream_t>(stream));
+}
+
+dspark_status dspark_page_trim(const int32_t* cur_len, const int32_t* keep_len, int R,
+                               int page_size, int max_pages, int num_pages,
+                               const int32_t* block_table, int32_t* ring,
+                               const dspark_page_pool* pool, dspark_page_pool* pool_out,
+                               void* stream) {
+  dspark::clear_error();
+  if (!cur_len || !keep_len || !block_table || !ring || !pool || !pool_out)
+    return fail(DSPARK_EINVAL, "page_trim: NULL required pointer");
+  if (R <= 0) return fail(DSPARK_EINVAL, "page_trim: R must be positive");
+  const dspark_status st = dspark::check_pages("page_trim", page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  if (pool == pool_out) return fail(DSPARK_EINVAL, "page_trim: pool_out needs its own address");
+  if (R > DSPARK_MAX_PAGE_REQUESTS)
+    return fail(DSPARK_EUNSUPPORTED, "page_trim: more than %d requests", DSPARK_MAX_PAGE_REQUESTS);
+  return dspark::launch_page_trim(cur_len, keep_len, R, dspark::page_shift(page_size), max_pages,
+                                  num_pages, block_table, ring, pool, pool_out,
+                                  reinterpret_cast<hipStream_t>(stream));
+}
+
+dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                              int dtype, const int64_t* slots, const int32_t* count,
+                              int max_tokens, int Hk, int D, int page_size, int num_pages,
+                              int cache_dtype, const float* k_scale, const float* v_scale,
+                              void* k_cache, void* v_cache, void* stream) {
+  dspark::clear_error();
+  if (!k || !v || !slots || !k_cache || !v_cache)
+    return fail(DSPARK_EINVAL, "kv_store: NULL required pointer");
+  if (max_tokens <= 0 || Hk <= 0 || D <= 0)
+    return fail(DSPARK_EINVAL, "kv_store: sizes must be positive");
+  dspark_status st = dspark::check_pages("kv_store", page_size, 1, num_pages);
+  if (st != DSPARK_OK) return st;
+  st = dspark::check_cache_types("kv_store", dtype, cache_dtype, k_scale, v_scale);
+  if (st != DSPARK_OK) return st;
+  if (!dspark::head_dim_ok(D) || Hk > 65535)
+    return fail(DSPARK_EUNSUPPORTED, "kv_store: D must be 64, 96, 128, 192 or 256 and Hk <= 65535");
+  if (k_stride % 8 || v_stride % 8 || k_stride < (int64_t)Hk * D || v_stride < (int64_t)Hk * D ||
+      !dspark::aligned(k, 16) || !dspark::aligned(v, 16) || !dspark::aligned(k_cache, 16) ||
+      !dspark::aligned(v_cache, 16))
+    return fail(DSPARK_EINVAL, "kv_store: rows and caches must be 16-byte aligned, rows at least "
+                               "Hk * D apart");
+  return dspark::launch_kv_store(k, v, k_stride, v_stride, dtype, slots, count, max_tokens, Hk, D,
+                                 dspark::page_shift(page_size), num_pages, cache_dtype, k_scale,
+                                 v_scale, k_cache, v_cache, reinterpret_cast<hipStream_t>(stream));
+}
+
+dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
+                               int64_t v_layer_stride, int layers, int cache_dtype,
+                               const int32_t* block_table, const int32_t* ctx_len,
+                               const int32_t* path, const int32_t* accepted, int R, int max_nodes,
+                               int Hk, int D, int page_size, int max_pages, int num_pages,
+                               int32_t* new_len, void* stream) {
+  dspark::clear_error();
+  if (!k_cache || !v_cache || !block_table || !ctx_len || !path || !accepted || !new_len)
+    return fail(DSPARK_EINVAL, "kv_commit: NULL required pointer");
+  if (R <= 0 || max_nodes <= 0 || Hk <= 0 || D <= 0 || layers <= 0)
+    return fail(DSPARK_EINVAL, "kv_commit: sizes must be positive");
+  const dspark_status st = dspark::check_pages("kv_commit", page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  if (cache_dtype != DSPARK_BF16 && cache_dtype != DSPARK_FP16 && cache_dtype != DSPARK_E4M3)
+    return fail(DSPARK_EINVAL, "kv_commit: unknown cache type %d", cache_dtype);
+  if (!dspark::head_dim_ok(D) || layers > 65535 || R > 65535)
+    return fail(DSPARK_EUNSUPPORTED, "kv_commit: D must be 64, 96, 128, 192 or 256, layers and R "
+                                     "<= 65535");
+  const int el = cache_dtype == DSPARK_E4M3 ? 1 : 2;
+  if (!dspark::aligned(k_cache, 16) || !dspark::aligned(v_cache, 16) ||
+      (k_layer_stride * el) % 16 || (v_layer_stride * el) % 16)
+    return fail(DSPARK_EINVAL, "kv_commit: caches and layers must be 16-byte aligned");
+  return dspark::launch_kv_commit(k_cache, v_cache, k_layer_stride, v_layer_stride, layers, el,
+                                  block_table, ctx_len, path, accepted, R, max_nodes, Hk, D,
+                                  dspark::page_shift(page_size), max_pages, num_pages, new_len,
+                                  reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, int D) {
+  if (R <= 0 || max_tokens <= 0 || Hq <= 0 || Hk <= 0 || Hq % Hk || !dspark::head_dim_ok(D))
+    return 0;
+  if (R > (1 << 20) || (int64_t)max_tokens * Hq > 0x7fffffffLL) return 0;
+  return dspark::tree_attention_workspace_bytes(R, max_tokens, Hq, Hk, D);
+}
+
+dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
+                                    const void* k_cache, const void* v_cache, int cache_dtype,
+                                    const float* k_scale, const float* v_scale,
+                                    const int32_t* block_table, const int32_t* ctx_len,
+                                    const int32_t* cu_seqlens, const uint32_t* tree_mask,
+                                    int mask_words, int R, int max_tokens, int Hq, int Hk, int D,
+                                    int page_size, int max_pages, int num_pages, float scale,
+                                    void* out, int64_t out_stride, float* lse, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  dspark::clear_error();
+  if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !cu_seqlens || !out)
+    return fail(DSPARK_EINVAL, "tree_attention: NULL required pointer");
+  if (R <= 0 || max_tokens <= 0 || Hq <= 0 || Hk <= 0 || D <= 0)
+    return fail(DSPARK_EINVAL, "tree_attention: sizes must be positive");
+  if (Hq % Hk) return fail(DSPARK_EINVAL, "tree_attention: Hq must be a multiple of Hk");
+  if (tree_mask ? mask_words <= 0 : mask_words != 0)
+    return fail(DSPARK_EINVAL, "tree_attention: mask_words goes with tree_mask");
+  if (!isfinite(scale)) return fail(DSPARK_EINVAL, "tree_attention: scale must be finite");
+  dspark_status st = dspark::check_pages("tree_attention", page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  st = dspark::check_cache_types("tree_attention", dtype, cache_dtype, k_scale, v_scale);
+  if (st != DSPARK_OK) return st;
+  const int64_t row = (int64_t)Hq * D;
+  if (!dspark::aligned(q, 16) || !dspark::aligned(out, 16) || !dspark::aligned(k_cache, 16) ||
+      !dspark::aligned(v_cache, 16) || q_stride % 8 || out_stride % 8 || q_stride < row ||
+      out_stride < row)
+    return fail(DSPARK_EINVAL, "tree_attention: rows and caches must be 16-byte aligned, rows at "
+                               "least Hq * D apart");
+  if (!dspark::head_dim_ok(D))
+    return fail(DSPARK_EUNSUPPORTED, "tree_attention: D must be 64, 96, 128, 192 or 256 (got %d)", D);
+  if (mask_words > DSPARK_MAX_MASK_WORDS)
+    return fail(DSPARK_EUNSUPPORTED, "tree_attention: mask rows above %d words", DSPARK_MAX_MASK_WORDS);
+  if (R > (1 << 20) || (int64_t)max_tokens * Hq > 0x7fffffffLL)
+    return fail(DSPARK_EUNSUPPORTED, "tree_attention: R above 2^20 or max_tokens * Hq above 2^31 - 1");
+  const size_t need = dspark::tree_attention_workspace_bytes(R, max_tokens, Hq, Hk, D);
+  if (!workspace || ws_bytes < need)
+    return fail(DSPARK_EWORKSPACE, "tree_attention: workspace needs %zu bytes (got %zu)", need,
+                workspace ? ws_bytes : (size_t)0);
+  if (!dspark::aligned(workspace, 256))
+    return fail(DSPARK_EINVAL, "tree_attention: workspace must be 256-byte aligned");
+  dspark::TreeAttnArgs a;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = block_table;
+  a.ctx = ctx_len;
+  a.cu = cu_seqlens;
+  a.mask = tree_mask;
+  a.out = out;
+  a.lse = lse;
+  a.ws = workspace;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.dtype = dtype;
+  a.cache_dtype = cache_dtype;
+  a.mask_words = mask_words;
+  a.R = R;
+  a.max_tokens = max_tokens;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.D = D;
+  a.shift = dspark::page_shift(page_size);
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.scale2 = (float)((double)scale * 1.4426950408889634);
+  return dspark::launch_tree_attention(a, reinterpret_cast<hipStream_t>(stream));
+}
+
+dspark_status dspark_tree_pack(const int32_t* parents, const int32_t* cu_seqlens,
+                               const int32_t* pos0, int R, int max_tokens, int mask_words,
+                               uint32_t* mask, int32_t* flat_pos, int32_t* flat_req,
+                               void* stream) {
+  dspark::clear_error();
+  if (!parents || !cu_seqlens || !mask)
+    return fail(DSPARK_EINVAL, "tree_pack: NULL required pointer");
+  if (R <= 0 || max_tokens <= 0 || mask_words <= 0)
+    return fail(DSPARK_EINVAL, "tree_pack: sizes must be positive");
+  if (mask_words > DSPARK_MAX_MASK_WORDS)
+    return fail(DSPARK_EUNSUPPORTED, "tree_pack: mask rows above %d words", DSPARK_MAX_MASK_WORDS);
+  return dspark::launch_tree_pack(parents, cu_seqlens, pos0, R, max_tokens, mask_words, mask,
+                                  flat_pos, flat_req, reinterpret_cast<hipStream_t>(stream));
+}
+
+dspark_status dspark_verify_tree(const float* target_logits, const int32_t* cu_seqlens,
+                                 const int32_t* tokens, const int32_t* parents, int R,
+                                 int max_tokens, int max_nodes, int V, int32_t* target_argmax,
+                                 int32_t* accepted, int32_t* path, int32_t* next_token,
+                                 void* stream) {
+  dspark::clear_error();
+  if (!target_logits || !cu_seqlens || !tokens || !parents || !target_argmax || !accepted ||
+      !path || !next_token)
+    return fail(DSPARK_EINVAL, "verify_tree: NULL required pointer");
+  if (R <= 0 || max_tokens <= 0 || max_nodes <= 0 || V < 1)
+    return fail(DSPARK_EINVAL, "verify_tree: sizes must be positive");
+  return dspark::launch_verify_tree(target_logits, cu_seqlens, tokens, parents, R, max_tokens,
+                                    max_nodes, V, target_argmax, accepted, path, next_token,
+                                    reinterpret_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

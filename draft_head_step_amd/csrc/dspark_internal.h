@@ -12,8 +12,14 @@ namespace dspark {
 // Sets the thread-local error text and returns `st`.
 dspark_status fail(dspark_status st, const char* fmt, ...);
 
+// Empties the thread-local error text.
+void clear_error();
+
 // Maps a HIP error (e.g. from hipGetLastError after a launch) to a status.
 dspark_status check_launch(const char* what);
+
+// Lets `kernel` use `bytes` of dynamic LDS on the current device.
+dspark_status allow_lds(const void* kernel, int bytes, const char* what);
 
 // ---- Markov-head step (fused gather + MFMA bias GEMM + bias-add + select) ----
 
@@ -121,6 +127,60 @@ dspark_status launch_verify_greedy(const float* target_logits, const int32_t* cu
                                    int32_t* next_token, hipStream_t stream);
 dspark_status launch_accept_prob(const float* draft_logits, const float* target_logits, int n,
                                  int V, float temperature, float* out, hipStream_t stream);
+
+// t_e = argmax of logits row e for e < n_rows[0] (a device count), rows at most `rows`.
+dspark_status launch_row_argmax(const float* logits, const int32_t* n_rows, int rows, int V,
+                                int32_t* amax, hipStream_t stream);
+
+// ---- verification over a paged cache ----
+dspark_status launch_page_map(const int32_t* cur_len, const int32_t* cu, int R, int max_tokens,
+                              int shift, int max_pages, int num_pages, int32_t* table,
+                              const int32_t* ring, const dspark_page_pool* pool,
+                              dspark_page_pool* pool_out, int64_t* slots, int32_t* new_len,
+                              hipStream_t stream);
+dspark_status launch_page_trim(const int32_t* cur_len, const int32_t* keep_len, int R, int shift,
+                               int max_pages, int num_pages, const int32_t* table, int32_t* ring,
+                               const dspark_page_pool* pool, dspark_page_pool* pool_out,
+                               hipStream_t stream);
+dspark_status launch_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                              int dtype, const int64_t* slots, const int32_t* count,
+                              int max_tokens, int Hk, int D, int shift, int num_pages,
+                              int cache_dtype, const float* k_scale, const float* v_scale,
+                              void* k_cache, void* v_cache, hipStream_t stream);
+dspark_status launch_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
+                               int64_t v_layer_stride, int layers, int bytes_per_element,
+                               const int32_t* block_table, const int32_t* ctx_len,
+                               const int32_t* path, const int32_t* accepted, int R, int max_nodes,
+                               int Hk, int D, int shift, int max_pages, int num_pages,
+                               int32_t* new_len, hipStream_t stream);
+// Arguments of the tree attention's kernels.
+struct TreeAttnArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* cu;
+  const uint32_t* mask;
+  void* out;
+  float* lse;
+  void* ws;
+  int64_t q_stride, out_stride;
+  int dtype, cache_dtype;
+  int mask_words, R, max_tokens, Hq, Hk, D, shift, max_pages, num_pages;
+  float scale2;   // scale * log2(e)
+};
+size_t tree_attention_workspace_bytes(int R, int max_tokens, int Hq, int Hk, int D);
+dspark_status launch_tree_attention(const TreeAttnArgs& a, hipStream_t stream);
+dspark_status launch_tree_pack(const int32_t* parents, const int32_t* cu, const int32_t* pos0,
+                               int R, int max_tokens, int mask_words, uint32_t* mask,
+                               int32_t* flat_pos, int32_t* flat_req, hipStream_t stream);
+dspark_status launch_verify_tree(const float* logits, const int32_t* cu, const int32_t* tokens,
+                                 const int32_t* parents, int R, int max_tokens, int max_nodes,
+                                 int V, int32_t* amax, int32_t* accepted, int32_t* path,
+                                 int32_t* next_token, hipStream_t stream);
 
 // ---- prefix scheduler ----
 dspark_status check_schedule_sizes(int R, int gamma, int B_max, bool uses_sps, const char* who);

@@ -14,6 +14,7 @@
 //                  (16-byte loads, per-thread running max in increasing v,
 //                  smallest id on ties), then one thread per request walks
 //                  its drafts against those argmaxes;
+//   verify_tree:   the same argmaxes, then one wave per request walks its tree;
 //   accept_prob:   one workgroup per row pair, two passes over V in base 2:
 //                  online (max, sum of 2^x) of both rows, four values per
 //                  rescale, then sum_v min(p, q).  With aligned rows (V a
@@ -223,6 +224,48 @@ __global__ __launch_bounds__(kRowT) void verify_argmax_kernel(const float* __res
   if (t == 0) {
     for (int j = 1; j < kRowW; ++j) take(bv, bi, sv[j], si[j]);
     amax[row] = bi < V ? bi : 0;
+  }
+}
+
+// Tree form of the walk: one wave per request.  From node `at` the next node is
+// the lowest-numbered one behind it (a child's number is larger than its
+// parent's) whose parent is `at` and whose token is the target's after `at`:
+// 64 nodes are tried at a time, the lowest set bit of the wave's vote is taken.
+__global__ __launch_bounds__(64) void verify_walk_kernel(
+    const int32_t* __restrict__ amax, const int32_t* __restrict__ cu,
+    const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents, int max_tokens,
+    int max_nodes, int32_t* __restrict__ accepted, int32_t* __restrict__ path,
+    int32_t* __restrict__ next_token) {
+  const int r = blockIdx.x;
+  const int lane = threadIdx.x;
+  const int32_t s = cu[r];
+  const int64_t end = min((int64_t)cu[r + 1], (int64_t)max_tokens);
+  int64_t len = s < 0 ? 0 : end - s;
+  const int n = (int)(len < 0 ? 0 : len > max_nodes ? max_nodes : len);
+  int32_t* row = path + (size_t)r * max_nodes;
+  int count = 0;       // nodes on the path
+  int32_t t = -1;
+  int at = 0;
+  bool found = n > 0;
+  while (found) {
+    if (lane == 0) row[count] = at;
+    ++count;
+    t = amax[s + at];
+    found = false;
+    for (int b = (at + 1) & ~63; b < n && !found; b += 64) {
+      const int c = b + lane;
+      const bool hit = c > at && c < n && parents[s + c] == at && tokens[s + c] == t;
+      const unsigned long long vote = __ballot(hit);
+      if (vote) {
+        at = b + __ffsll(vote) - 1;
+        found = true;
+      }
+    }
+  }
+  for (int i = count + lane; i < max_nodes; i += 64) row[i] = -1;
+  if (lane == 0) {
+    accepted[r] = count - 1;
+    next_token[r] = t;
   }
 }
 
@@ -562,14 +605,33 @@ dspark_status launch_verify_pack(const int32_t* anchors, const int32_t* tokens,
   return check_launch("verify_pack");
 }
 
+dspark_status launch_row_argmax(const float* logits, const int32_t* n_rows, int rows, int V,
+                                int32_t* amax, hipStream_t stream) {
+  const int vec = (V % 4 == 0) && ((reinterpret_cast<uintptr_t>(logits) & 15u) == 0);
+  hipLaunchKernelGGL(verify_argmax_kernel, dim3(rows), dim3(kRowT), 0, stream, logits, n_rows, 0,
+                     V, vec, amax);
+  return check_launch("verify_argmax_kernel");
+}
+
+dspark_status launch_verify_tree(const float* logits, const int32_t* cu, const int32_t* tokens,
+                                 const int32_t* parents, int R, int max_tokens, int max_nodes,
+                                 int V, int32_t* amax, int32_t* accepted, int32_t* path,
+                                 int32_t* next_token, hipStream_t stream) {
+  const dspark_status st = launch_row_argmax(logits, cu + R, max_tokens, V, amax, stream);
+  if (st != DSPARK_OK) return st;
+  hipLaunchKernelGGL(verify_walk_kernel, dim3(R), dim3(64), 0, stream, amax, cu, tokens, parents,
+                     max_tokens, max_nodes, accepted, path, next_token);
+  return check_launch("verify_walk_kernel");
+}
+
 dspark_status launch_verify_greedy(const float* target_logits, const int32_t* cu_seqlens,
                                    const int32_t* tokens, int R, int gamma, int V,
                                    int32_t* target_argmax, int32_t* accepted,
                                    int32_t* next_token, hipStream_t stream) {
   const int rows = R * (1 + gamma);
-  const int vec = (V % 4 == 0) && ((reinterpret_cast<uintptr_t>(target_logits) & 15u) == 0);
-  hipLaunchKernelGGL(verify_argmax_kernel, dim3(rows), dim3(kRowT), 0, stream, target_logits,
-                     cu_seqlens, R, V, vec, target_argmax);
+  const dspark_status st = launch_row_argmax(target_logits, cu_seqlens + R, rows, V, target_argmax,
+                                             stream);
+  if (st != DSPARK_OK) return st;
   hipLaunchKernelGGL(verify_accept_kernel, dim3((R + 255) / 256), dim3(256), 0, stream,
                      target_argmax, cu_seqlens, tokens, R, gamma, accepted, next_token);
   return check_launch("verify_greedy");

@@ -443,6 +443,242 @@ dspark_status dspark_verify_greedy(const float* target_logits, const int32_t* cu
 dspark_status dspark_accept_prob(const float* draft_logits, const float* target_logits, int n,
                                  int V, float temperature, float* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Verification over a paged key/value cache: the target engine's side of the
+ * step between the flattened batch and its logits.  [P1] section 三 challenge
+ * 3: every verified token is one flattened element, and the attention takes
+ * the dependencies inside a sequence from a marker tensor.  The pages give no
+ * kernels or layouts for it; these are this library's own.
+ *
+ * Request r has ctx_len[r] tokens in the cache and brings the elements
+ * cu_seqlens[r] .. cu_seqlens[r+1] - 1 of the flattened batch (n_r of them: an
+ * anchor and its drafts), as a chain or as a tree.  Element j of the segment
+ * (0-based) is kept at cache position ctx_len[r] + j.
+ *
+ * Pages.  Position p of request r lies in page block_table[r, p / P] at offset
+ * p % P, P = page_size a power of two in [16, 1024]; a slot is
+ * page * P + offset (int64).  block_table is [R, max_pages] int32; entries
+ * behind a request's last page are neither read nor written.
+ *
+ * Cache.  For Hk heads of D values and c = 16 / (bytes per element):
+ *     k_cache [num_pages][Hk][D / c][P][c]     element (page, h, d, o) at
+ *             (((page * Hk + h) * (D / c) + d / c) * P + o) * c + d % c
+ *     v_cache [num_pages][Hk][D][P]            ((page * Hk + h) * D + d) * P + o
+ * Both are the operand order of the matrix instructions, so a 16-byte load of
+ * either feeds them without a transpose.  DSPARK_E4M3 caches hold x / scale in
+ * OCP e4m3 (finite values up to 448) with one scale per head for the keys and
+ * one for the values.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the cache calls. */
+typedef enum {
+  DSPARK_BF16 = 0,
+  DSPARK_FP16 = 1,
+  DSPARK_E4M3 = 2 /* caches only */
+} dspark_dtype;
+
+#define DSPARK_MAX_PAGE_REQUESTS 16384 /* R of dspark_page_map / dspark_page_trim */
+#define DSPARK_MAX_MASK_WORDS 32       /* 32-bit words of a tree mask row: 1024 nodes */
+
+/* State of a ring of free pages, in DEVICE memory (16 bytes).  The free pages
+ * are ring[(head + i) mod num_pages] for 0 <= i < count.  A new pool of n pages
+ * is ring = 0, 1, ..., n - 1 with head = 0 and count = n. */
+typedef struct {
+  int32_t head;
+  int32_t count;
+  int32_t refused;  /* output: requests that the call turned down */
+  int32_t reserved; /* written as 0 */
+} dspark_page_pool;
+
+/*
+ * Pages and slots for the new elements of every request, from lengths that
+ * only the device knows.  With n_r = cu_seqlens[r+1] - cu_seqlens[r],
+ *     need_r = ceil((cur_len[r] + n_r) / P) - ceil(cur_len[r] / P),
+ *     S_r    = need_0 + ... + need_{r-1}
+ * request r is served if S_r + need_r <= count: its new pages are
+ *     block_table[r, ceil(cur_len[r] / P) + i] = ring[(head + S_r + i) mod num_pages]
+ * slots[cu_seqlens[r] + j] is the slot of position cur_len[r] + j and
+ * new_len[r] = cur_len[r] + n_r.  A request that is not served (the pool is
+ * short, cur_len[r] or n_r negative, or more than max_pages pages) leaves its
+ * block_table row as it was, gets slots of -1 and new_len[r] = cur_len[r], and
+ * counts in pool_out->refused; one that asks for no page is served whatever
+ * the pool holds, and one with too many pages takes none from the others.  A
+ * slot whose page id lies outside [0, num_pages) is -1.
+ *   cur_len     [R] int32 tokens that each request holds.
+ *   cu_seqlens  [R+1] int32 segment starts.
+ *   block_table [R, max_pages] int32, new entries written.
+ *   ring        [num_pages] int32 (read).
+ *   pool        device dspark_page_pool before the call (read).
+ *   pool_out    device dspark_page_pool after it; another address than pool, so
+ *               that a call can be repeated.
+ *   slots       [max_tokens] int64 output; entries from cu_seqlens[R] on are left
+ *               as they were, elements from max_tokens on get no slot.
+ *   new_len     [R] int32 output; another address than cur_len.
+ * One launch.  Errors: EINVAL for NULL pointers, sizes <= 0, a page size that
+ * is no power of two in [16, 1024], pool_out == pool or new_len == cur_len;
+ * EUNSUPPORTED for R > DSPARK_MAX_PAGE_REQUESTS; EDEVICE on a launch failure.
+ */
+dspark_status dspark_page_map(const int32_t* cur_len, const int32_t* cu_seqlens, int R,
+                              int max_tokens, int page_size, int max_pages, int num_pages,
+                              int32_t* block_table, const int32_t* ring,
+                              const dspark_page_pool* pool, dspark_page_pool* pool_out,
+                              int64_t* slots, int32_t* new_len, void* stream);
+
+/*
+ * Pages back to the pool: request r keeps keep_len[r] of its cur_len[r] tokens
+ * (keep_len is clamped into [0, cur_len]; 0 ends a request).  With
+ * give_r = ceil(cur_len[r] / P) - ceil(keep_len[r] / P) and S its running sum,
+ *     ring[(head + count + S_r + i) mod num_pages] = block_table[r, ceil(keep_len[r] / P) + i]
+ * and the pool's count grows by the sum.  block_table is not changed: the
+ * entries behind the last kept page are simply not read any more.
+ * A request with cur_len[r] < 0 or more than max_pages pages gives nothing and
+ * counts in pool_out->refused; if the ring would hold more than num_pages
+ * pages (pages given back twice) nothing is written to it and refused = R.
+ * One launch.  Errors: as dspark_page_map.
+ */
+dspark_status dspark_page_trim(const int32_t* cur_len, const int32_t* keep_len, int R,
+                               int page_size, int max_pages, int num_pages,
+                               const int32_t* block_table, int32_t* ring,
+                               const dspark_page_pool* pool, dspark_page_pool* pool_out,
+                               void* stream);
+
+/*
+ * Keys and values of new elements into their slots.
+ *   k, v        rows of [Hk, D] elements of `dtype` (BF16 or FP16), row e at
+ *               k + e * k_stride (strides in elements, multiples of 8, at least
+ *               Hk * D; bases 16-byte aligned).
+ *   slots       [max_tokens] int64 as dspark_page_map writes them; an element
+ *               whose slot lies outside [0, num_pages * P) is skipped.  The slots
+ *               of one call are distinct (of two elements with one slot, either
+ *               may be kept, value by value).
+ *   count       optional device int32: the number of elements (cu_seqlens + R);
+ *               NULL stands for max_tokens.
+ *   cache_dtype `dtype` itself, or DSPARK_E4M3.
+ *   k_scale, v_scale  [Hk] fp32 positive, required with DSPARK_E4M3 (NULL
+ *               otherwise): x / scale (fp32) is clamped to +-448 and rounded to
+ *               nearest even; NaN stays NaN.
+ * Errors: EINVAL for NULL pointers, sizes <= 0, bad types, page sizes, strides
+ * or alignment, scales missing or given without DSPARK_E4M3; EUNSUPPORTED for
+ * D outside {64, 96, 128, 192, 256} or Hk > 65535; EDEVICE.
+ */
+dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                              int dtype, const int64_t* slots, const int32_t* count,
+                              int max_tokens, int Hk, int D, int page_size, int num_pages,
+                              int cache_dtype, const float* k_scale, const float* v_scale,
+                              void* k_cache, void* v_cache, void* stream);
+
+/*
+ * The accepted path to the front: for i = 1 .. accepted[r] the keys and values
+ * at position ctx_len[r] + path[r, i] move to position ctx_len[r] + i, and
+ * new_len[r] = ctx_len[r] + 1 + accepted[r].  accepted[r] = -1 (a request
+ * without elements) moves nothing and gives new_len[r] = ctx_len[r].
+ *   k_cache, v_cache  caches of `layers` layers, layer l at l * k_layer_stride
+ *               (v_layer_stride) elements (multiples of 16 / element size).
+ *   path        [R, max_nodes] int32: 0, then strictly increasing node numbers (as
+ *               dspark_verify_tree writes them).
+ * A request whose path is not such a sequence, whose accepted count lies
+ * outside [-1, max_nodes), or that touches a page id outside [0, num_pages) or
+ * a position past its table moves nothing and gets new_len[r] = -1.
+ * Errors: EINVAL for NULL pointers, sizes <= 0, a bad page size or type,
+ * misaligned caches or strides; EUNSUPPORTED for D as above, layers > 65535 or
+ * R > 65535; EDEVICE.
+ */
+dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
+                               int64_t v_layer_stride, int layers, int cache_dtype,
+                               const int32_t* block_table, const int32_t* ctx_len,
+                               const int32_t* path, const int32_t* accepted, int R, int max_nodes,
+                               int Hk, int D, int page_size, int max_pages, int num_pages,
+                               int32_t* new_len, void* stream);
+
+/* Bytes of workspace dspark_tree_attention needs (0 if invalid).  It depends on
+ * the current device's number of compute units. */
+size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, int D);
+
+/*
+ * Attention of every element over its request's context and over the elements
+ * of its own segment that its mask names.  For element i of request r and
+ * query head y (key/value head h = y / (Hq / Hk)):
+ *     s_t  = scale * k_scale[h] * sum_d q[e, y, d] k[t, h, d]
+ *     out  = sum_t softmax(s)_t * v_scale[h] v[t, h, :]
+ *     lse  = ln sum_t exp(s_t)
+ * over the positions t < ctx_len[r] and t = ctx_len[r] + j with j visible to i:
+ * j <= i where tree_mask is NULL (a chain), else bit j % 32 of
+ * tree_mask[e, j / 32] (bits past the segment or past mask_words are not set).
+ * A row that sees nothing gives out = 0 and lse = -inf; positions that a row
+ * does not see do not reach it, whatever their keys and values hold.
+ * Products take the element type with fp32 accumulation (e4m3 keys and values
+ * are widened first, exactly); scores, maxima and sums are fp32; each
+ * probability is rounded to the element type before it meets the values.
+ *   q           rows of [Hq, D] elements of `dtype`, row e at q + e * q_stride
+ *               (elements; a multiple of 8, base 16-byte aligned).
+ *   ctx_len     [R] int32; cu_seqlens [R+1] int32.  Rows from
+ *               min(cu_seqlens[R], max_tokens) on are neither read nor written.
+ *   tree_mask   [max_tokens, mask_words] uint32 or NULL (mask_words is then 0).
+ *   k_scale, v_scale  [Hk] fp32 with a DSPARK_E4M3 cache, NULL otherwise.
+ *   scale       finite.
+ *   out         rows of [Hq, D] elements of `dtype`, row e at out + e * out_stride.
+ *   lse         optional [max_tokens, Hq] fp32.
+ *   workspace   >= dspark_tree_attention_workspace(...) bytes, 256-byte aligned;
+ *               its contents on entry do not matter.
+ * Every row of a request with ctx_len[r] < 0, more positions than its table
+ * has, or a page id outside [0, num_pages) among those that it reads is NaN.
+ * The sums are split in a fixed way, so results do not vary between runs.
+ * Errors: EINVAL for NULL pointers, sizes <= 0, Hq not a multiple of Hk, bad
+ * types, page sizes, strides, alignment or scale, scales missing or given
+ * without DSPARK_E4M3; EUNSUPPORTED for D outside {64, 96, 128, 192, 256},
+ * mask_words > DSPARK_MAX_MASK_WORDS, R > 2^20 or max_tokens * Hq above 2^31 - 1;
+ * EWORKSPACE; EDEVICE.
+ */
+dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
+                                    const void* k_cache, const void* v_cache, int cache_dtype,
+                                    const float* k_scale, const float* v_scale,
+                                    const int32_t* block_table, const int32_t* ctx_len,
+                                    const int32_t* cu_seqlens, const uint32_t* tree_mask,
+                                    int mask_words, int R, int max_tokens, int Hq, int Hk, int D,
+                                    int page_size, int max_pages, int num_pages, float scale,
+                                    void* out, int64_t out_stride, float* lse, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
+/*
+ * A forest of drafted nodes in the form that the attention reads.  parents[e]
+ * is the segment-local number of element e's parent, smaller than its own, or
+ * -1 for a root.
+ *   mask      [max_tokens, mask_words] uint32 output: bits of the element itself
+ *             and of its ancestors.
+ *   flat_pos  optional [max_tokens] int32 output: pos0[r] + depth (pos0 [R] int32,
+ *             0 if NULL).
+ *   flat_req  optional [max_tokens] int32 output: the request.
+ * An element with a parent outside [-1, own number) on its way to the root, or
+ * with a number of 32 * mask_words or more, gets an empty mask row and
+ * position -1.  Rows from cu_seqlens[R] on are left as they were.
+ * Errors: EINVAL for NULL pointers or sizes <= 0; EUNSUPPORTED for mask_words >
+ * DSPARK_MAX_MASK_WORDS; EDEVICE.
+ */
+dspark_status dspark_tree_pack(const int32_t* parents, const int32_t* cu_seqlens,
+                               const int32_t* pos0, int R, int max_tokens, int mask_words,
+                               uint32_t* mask, int32_t* flat_pos, int32_t* flat_req, void* stream);
+
+/*
+ * Greedy verification of trees: dspark_verify_greedy where every segment is a
+ * tree whose node 0 is the anchor.  t_e = argmax_v of target_logits row e (ties
+ * to the smallest id; rows free of NaN).  The walk starts at node 0 and goes
+ * from a node to its lowest-numbered child whose token is the node's t, as long
+ * as there is one.
+ *   target_logits  [max_tokens, V] fp32; rows from cu_seqlens[R] on are not read.
+ *   tokens, parents  [max_tokens] int32 flattened (the anchor's token is not read).
+ *   max_nodes      nodes of a segment that are looked at, and columns of path.
+ *   target_argmax  [max_tokens] int32 output (the first cu_seqlens[R] are written).
+ *   accepted       [R] int32 output: drafts accepted (-1 for an empty segment).
+ *   path           [R, max_nodes] int32 output: 0, the accepted nodes, then -1.
+ *   next_token     [R] int32 output: t of the last node on the path (-1 if empty).
+ * Errors: EINVAL for NULL pointers or sizes <= 0; EDEVICE.
+ */
+dspark_status dspark_verify_tree(const float* target_logits, const int32_t* cu_seqlens,
+                                 const int32_t* tokens, const int32_t* parents, int R,
+                                 int max_tokens, int max_nodes, int V, int32_t* target_argmax,
+                                 int32_t* accepted, int32_t* path, int32_t* next_token,
+                                 void* stream);
+
 /* Static description of a status code. */
 const char* dspark_status_string(int status);
 
