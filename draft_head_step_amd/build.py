@@ -28,7 +28,8 @@ SOURCES = ["api.hip", "markov_step.hip", "markov_pick_greedy_row.hip", "markov_p
            "markov_pick_sample_row.hip", "markov_pick_sample_col.hip", "markov_pick_bias_only.hip",
            "confidence.hip", "schedule.hip", "verify.hip", "noalloc.hip", "rnn_head.hip",
            "layout.hip", "api_paged.hip", "pages.hip", "kv_cache.hip", "tree_pack.hip",
-           "tree_attention.hip"]
+           "tree_attention.hip", "tree_attention_bf16.hip", "tree_attention_fp16.hip",
+           "tree_attention_bf16_e4m3.hip", "tree_attention_fp16_e4m3.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,0 +1,820 @@
+// Kernels of the attention of drafted elements over a paged cache (gfx950).
+//
+// With x_t = scale log2(e) k_scale q . k_t and m >= max x_t - kSlack a running
+// reference, a row keeps l = sum 2^(x_t - m) and O = sum 2^(x_t - m) v_t: one
+// pass over the cache, rescaled when a new maximum leaves m more than kSlack
+// behind (so that most steps rescale nothing; the exponent range of fp32 sums and
+// of both 16-bit types holds 2^kSlack).
+//
+// Both products run on the matrix cores transposed, S^T = K Q^T and O^T = V^T P^T:
+// a step's positions are the rows of the first result and the contraction of
+// the second, and a query row is a matrix column, so a lane holds one row's
+// scores, its maximum and its rescale factor, and what the first product leaves
+// in a lane is what the second one takes there.  Nothing crosses lanes but the
+// row maximum (two lane swaps).  The caches are stored in operand order, so keys
+// and values go from memory to registers to the matrix cores, 16 bytes a lane,
+// with no LDS on the way.
+//
+// A step is kTok positions: 4 groups (lane / 16) of c = 16 / element size
+// neighbouring positions.  Row 4 g + i of key tile kt is position c g + 4 kt + i:
+// the scores that a lane gets are those of its own group's c positions, in the
+// order in which its 16 bytes of a value channel hold them.
+//
+// Work is split by length, not by request: the row tiles of all requests and
+// heads are laid end to end in units of (waves over positions) * kTok positions,
+// and each workgroup takes an equal run of units, whatever requests it
+// crosses.  A tile cut by a run's end goes to the workspace in parts (fp32), and
+// a second launch joins them.  Each workgroup finds its place by scanning the
+// lengths itself.
+//
+// A workgroup's four waves share a tile of 16 NT WR rows: WR waves over rows,
+// 4 / WR over positions (interleaved steps).  A request's rows are cut into tiles
+// with WR = 4 and a last one whose WR goes by what is left, so that a chain of a
+// few drafts spreads over positions and a wide tree reads its cache once.
+//
+// Pages of at least a step's positions are the same for a whole wave: their
+// addresses are scalars (kPage = 0).  Smaller ones differ between lane groups:
+// there the page size is a constant, and so are the distances between a
+// lane's loads (kPage = log2 of the page size).
+#pragma once
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "dspark_internal.h"
+#include "paged.h"
+
+namespace dspark {
+
+// A tile that a workgroup's run ends in: its parts are slot 2 * b + 1 of this
+// workgroup b and slots 2 * (b + 1), 2 * (b + 2), ... of the next ones.
+struct AttnCut {
+  int32_t r, h, row_tile, parts;   // parts = 0: none
+};
+
+struct AttnPlan {
+  int groups;       // workgroups
+  int nt;           // 16-row tiles per wave
+  int row_blocks;   // 16-row blocks of a part that may hold rows
+  size_t cut_bytes, ml_bytes, o_bytes;   // workspace: AttnCut[groups], (m, l), O
+};
+AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64_t capacity);
+
+template <int DT, bool F8>
+dspark_status run_tree_attention(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream);
+
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kSlack = 8.0f;
+
+// Operands and conversions of an element type (0 bf16, 1 fp16).
+template <int DT> struct El;
+template <> struct El<0> {
+  static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const bf16x2 p = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  template <bool HI> static __device__ __forceinline__ uint32_t wide(uint32_t x) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, HI));
+  }
+};
+template <> struct El<1> {
+  static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const f16x2 p = {(_Float16)x, (_Float16)y};
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  template <bool HI> static __device__ __forceinline__ uint32_t wide(uint32_t x) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, HI));
+  }
+};
+
+// Half `s` of 16 e4m3 values as 8 elements; exact, both types hold every e4m3 value.
+template <int DT> __device__ __forceinline__ u32x4 widen8(u32x4 x, int s) {
+  u32x4 r;
+  r[0] = El<DT>::template wide<false>(x[2 * s]);
+  r[1] = El<DT>::template wide<true>(x[2 * s]);
+  r[2] = El<DT>::template wide<false>(x[2 * s + 1]);
+  r[3] = El<DT>::template wide<true>(x[2 * s + 1]);
+  return r;
+}
+
+// Flags of the two halves of a word, in bits 0 and 16: |half| >= limit (a half's
+// sign bit is free for the carry).
+__device__ __forceinline__ uint32_t halves_from(uint32_t x, uint32_t limit) {
+  return (((x & 0x7fff7fffu) + (0x8000u - limit) * 0x00010001u) >> 15) & 0x00010001u;
+}
+// Flags of the four bytes, in bits 0, 8, 16 and 24: e4m3 NaN.
+__device__ __forceinline__ uint32_t bytes_nan(uint32_t x) {
+  return (((x & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;
+}
+// Bit i of `bits` as a whole word of ones or zeros.
+__device__ __forceinline__ uint32_t spread(uint32_t bits, int i) {
+  return (uint32_t)((int32_t)(bits << (31 - i)) >> 31);
+}
+
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A bit cast of a vector's element reads element 0: elements are copied first.
+__device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
+__device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+
+// Over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float groups_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false);
+  x = fmaxf(as_float(a[0]), as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false);
+  return fmaxf(as_float(b[0]), as_float(b[1]));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// A request as the work split sees it.
+struct Req {
+  int start;        // its first element
+  int n;            // elements that are visible to each other
+  int rows;         // query rows to compute (elements within max_tokens, times heads a group)
+  int ctx, total;   // positions before the segment, and with it
+  int full;         // row tiles with four waves over rows
+  int wr_last;      // waves over rows of the last one, 0 if there is none
+  int units_full, units_last;   // units of a tile
+  bool bad;
+  __device__ __forceinline__ int64_t head_units() const {
+    return (int64_t)full * units_full + units_last;
+  }
+};
+template <int NT, int TOK>
+__device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) {
+  Req q;
+  const int64_t s = a.cu[r], e = a.cu[r + 1];
+  const int64_t n = s < 0 || e < s ? 0 : e - s;
+  const int64_t here = n < a.max_tokens - s ? n : a.max_tokens - s;
+  const int64_t ctx = a.ctx[r];
+  const int64_t total = ctx + n;
+  q.start = (int)s;
+  q.n = (int)n;
+  q.rows = here > 0 ? (int)here * group : 0;
+  q.bad = ctx < 0 || total > 0x7fff0000LL || pages_of(total < 0 ? 0 : total, a.shift) > a.max_pages;
+  q.ctx = q.bad ? 0 : (int)ctx;
+  q.total = q.bad ? 0 : (int)total;
+  constexpr int kTile = 16 * NT * kWaves;
+  q.full = q.rows / kTile;
+  const int rest = q.rows - q.full * kTile;
+  q.wr_last = rest == 0 ? 0 : rest <= 16 * NT ? 1 : rest <= 32 * NT ? 2 : 4;
+  const int steps = q.bad ? 1 : (q.total + TOK - 1) / TOK;
+  q.units_full = steps;
+  const int wt = q.wr_last ? kWaves / q.wr_last : 1;
+  q.units_last = q.wr_last ? (steps + wt - 1) / wt : 0;
+  return q;
+}
+
+// Waves of a SIMD that the registers of a tile allow.
+constexpr int attn_waves(int nt, int d) {
+  return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : nt * d <= 256 && d <= 128 ? 2 : 1;
+}
+
+// Launch with kThreads threads; a run of units per workgroup.
+template <int DT, bool F8, int D, int NT, int kPage>
+__global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_kernel(
+    const TreeAttnArgs a, AttnCut* __restrict__ cuts, float* __restrict__ part_ml,
+    float* __restrict__ part_o) {
+  constexpr int kC = F8 ? 16 : 8;        // positions of a lane's 16 bytes of values
+  constexpr int kTok = 4 * kC;           // positions of a step
+  constexpr int kKT = kC / 4;            // key tiles of a step
+  constexpr int kJ = F8 ? (D + 63) / 64 : D / 32;   // 16-byte key loads a tile
+  constexpr int kMj = F8 ? 2 : 1;        // products a key load feeds
+  constexpr int kU = kC / 8;             // products a value load feeds
+  constexpr int kDT = D / 16;            // output tiles
+  constexpr int kEl = F8 ? 1 : 2;
+  constexpr int kPieces = D / kC;        // 16-byte pieces of a key row
+  using E = El<DT>;
+
+  __shared__ f32x4 sh_o[2][NT * kDT][64];
+  __shared__ float sh_ml[2][NT][2][64];
+  __shared__ int64_t sh_scan[kWaves];
+  __shared__ int64_t sh_pos[2];          // request and unit within it of this run's first unit
+
+  const int t = threadIdx.x;
+  const int lane = t & 63;
+  const int wave = uni(t >> 6);
+  const int col = lane & 15;             // query row within a 16-row tile
+  const int g = lane >> 4;               // lane group
+  const int group = a.Hq / a.Hk;
+  const int G = gridDim.x;
+  // neighbouring runs on one XCD (workgroups go to the eight XCDs in turn)
+  const int b = (G & 7) == 0 ? (int)(blockIdx.x & 7) * (G >> 3) + (int)(blockIdx.x >> 3)
+                             : (int)blockIdx.x;
+
+  // ---- where this run starts ----
+  // With fewer units than workgroups each of the first ones takes one: every run
+  // between a tile's first and last part holds a part.
+  int64_t w, w_end, all, runs;
+  {
+    const int per = (a.R + kThreads - 1) / kThreads;
+    const int r0 = min(t * per, a.R), r1 = min(r0 + per, a.R);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok>(a, r, group).head_units();
+    int64_t inc = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t o = __shfl_up(inc, off);
+      inc += lane >= off ? o : 0;
+    }
+    if (lane == 63) sh_scan[wave] = inc;
+    __syncthreads();
+    int64_t pre = 0;
+    all = 0;
+#pragma unroll
+    for (int j = 0; j < kWaves; ++j) {
+      pre += j < wave ? sh_scan[j] : 0;
+      all += sh_scan[j];
+    }
+    runs = all < G ? all : G;
+    w = b < runs ? all * b / runs : 0;
+    w_end = b < runs ? all * (b + 1) / runs : 0;
+    int64_t first = pre + inc - mine;
+    if (w < w_end && w >= first && w < first + mine) {
+      for (int r = r0; r < r1; ++r) {
+        const int64_t u = a.Hk * request<NT, kTok>(a, r, group).head_units();
+        if (w < first + u) {
+          sh_pos[0] = r;
+          sh_pos[1] = w - first;
+          break;
+        }
+        first += u;
+      }
+    }
+    __syncthreads();
+  }
+  if (w >= w_end) {
+    if (t == 0) cuts[b] = AttnCut{0, 0, 0, 0};
+    return;
+  }
+  int r = uni((int)sh_pos[0]);
+  int64_t at = sh_pos[1];
+  AttnCut cut = {0, 0, 0, 0};
+
+  while (w < w_end) {
+    const Req rq = request<NT, kTok>(a, r, group);
+    const int64_t per_head = rq.head_units();
+    if (at >= a.Hk * per_head) {   // also requests without work
+      at -= a.Hk * per_head;
+      ++r;
+      continue;
+    }
+    // ---- this segment: units s0 .. s1 of row tile `row_tile` of head h ----
+    const int h = uni((int)(at / per_head));
+    const int64_t in_head = at - h * per_head;
+    const bool full = in_head < (int64_t)rq.full * rq.units_full;
+    const int row_tile = uni(full ? (int)(in_head / rq.units_full) : rq.full);
+    const int units = uni(full ? rq.units_full : rq.units_last);
+    const int wr = uni(full ? kWaves : rq.wr_last);
+    const int s0 = uni((int)(in_head - (int64_t)row_tile * rq.units_full));
+    const int64_t left = w_end - w;
+    const int s1 = uni((int)(left < units - s0 ? s0 + left : units));
+    const int wt = kWaves / wr;
+    const int my_t = wave / wr, my_r = wave & (wr - 1);
+    const int ctx = uni(rq.ctx), total = uni(rq.total);
+    const int row0 = row_tile * (16 * NT * kWaves) + my_r * 16 * NT;
+    const bool idle = row0 >= rq.rows;
+
+    const float ks = a.k_scale ? a.k_scale[h] : 1.0f;
+    float sc = a.scale2 * ks;
+    const uint32_t flip = sc < 0.0f ? 0x80008000u : 0u;   // the sign goes to the queries
+    sc = fabsf(sc);
+    u32x4 qf[NT][kJ * kMj];
+    int el[NT];                            // element (within the segment) of this lane's row
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 16 + col;
+      const bool in = row < rq.rows;
+      el[nt] = in ? row / group : 0;
+      const int y = in ? row - el[nt] * group : 0;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
+                           (int64_t)(rq.start + el[nt]) * a.q_stride + (h * group + y) * D;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int i = 0; i < kMj; ++i) {
+          const int d = F8 ? (j * 4 + g) * 16 + i * 8 : (j * 4 + g) * 8;
+          u32x4 x = {0, 0, 0, 0};
+          if (in && d < D) x = *reinterpret_cast<const u32x4*>(qp + d);
+          qf[nt][j * kMj + i] = x ^ flip;
+        }
+    }
+    f32x4 o[NT][kDT];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -INFINITY;
+      l[nt] = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < kDT; ++dt) o[nt][dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // the last position that a row of this wave sees, plus one
+    int seen = total;
+    if (!a.mask && !idle)
+      seen = min(seen, ctx + (min(rq.rows, row0 + 16 * NT) - 1) / group + 1);
+    bool bad = rq.bad;
+    const int t_step = kTok * wt;
+    int t0 = uni((s0 * wt + my_t) * kTok);
+    const int t_end = uni(idle || bad ? 0 : min(seen, s1 * t_step));
+
+    if (t0 < t_end) {
+      const int shift = kPage ? kPage : a.shift;
+      const int P = 1 << shift;
+      const int last_page = (total - 1) >> shift;
+      const int64_t page_bytes = ((int64_t)a.Hk * D << shift) * kEl;
+      const uint8_t* kh = static_cast<const uint8_t*>(a.k_cache) + ((int64_t)h * D << shift) * kEl;
+      const uint8_t* vh = static_cast<const uint8_t*>(a.v_cache) + ((int64_t)h * D << shift) * kEl;
+      const int kb = kC * (col >> 2);       // this lane's key rows start there within a step
+      const int vb = kC * g;                // and its values there
+      const int32_t* pages = a.table + (int64_t)r * a.max_pages;
+      u32x4 kf[kKT][kJ], vf[kDT];
+      // Page of this lane's keys (b = kb) or values (b = vb) of the step at tt; for
+      // kPage = 0 one scalar for the wave.  Entries are read two steps ahead of
+      // their use, keys and values one.
+      auto entry = [&](int tt, int bb) {
+        if constexpr (kPage == 0) {
+          typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+          return ((scalar_ptr)(uintptr_t)pages)[min(tt >> shift, last_page)];
+        } else {
+          return pages[min((tt + bb) >> shift, last_page)];
+        }
+      };
+      auto check = [&](int32_t p) {
+        const bool ok = page_ok(p, a.num_pages);
+        bad |= !ok;
+        return ok ? p : 0;
+      };
+      auto load_k = [&](int32_t page, int tt) {
+        if constexpr (kPage == 0) {
+          const uint8_t* base = kh + page * page_bytes + (tt & (P - 1)) * 16;
+          const uint32_t off = (uint32_t)((kb + (col & 3)) * 16 + g * (P * 16));
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            const uint8_t* bj = base + (int64_t)j * 4 * P * 16;
+#pragma unroll
+            for (int kt = 0; kt < kKT; ++kt) {
+              const bool none = kPieces % 4 != 0 && j * 4 + g >= kPieces;
+              kf[kt][j] = *reinterpret_cast<const u32x4*>(bj + (none ? off - g * (P * 16) : off) + kt * 64);
+              if (none) kf[kt][j] = u32x4{0, 0, 0, 0};
+            }
+          }
+        } else {
+          const uint8_t* base = kh + page * page_bytes + (((tt + kb) & (P - 1)) + (col & 3)) * 16 +
+                                g * (P * 16);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int kt = 0; kt < kKT; ++kt) {
+              const bool none = kPieces % 4 != 0 && j * 4 + g >= kPieces;
+              kf[kt][j] = *reinterpret_cast<const u32x4*>(base - (none ? g * (P * 16) : 0) +
+                                                          j * 4 * P * 16 + kt * 64);
+              if (none) kf[kt][j] = u32x4{0, 0, 0, 0};
+            }
+        }
+      };
+      auto load_v = [&](int32_t page, int tt) {
+        if constexpr (kPage == 0) {
+          const uint8_t* base = vh + page * page_bytes + (tt & (P - 1)) * kEl;
+          const uint32_t off = (uint32_t)((col * P + vb) * kEl);
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt)
+            vf[dt] = *reinterpret_cast<const u32x4*>(base + (int64_t)dt * 16 * P * kEl + off);
+        } else {
+          const uint8_t* base = vh + page * page_bytes + (col * P + ((tt + vb) & (P - 1))) * kEl;
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt)
+            vf[dt] = *reinterpret_cast<const u32x4*>(base + dt * 16 * P * kEl);
+        }
+      };
+      int32_t pk = check(entry(t0, kb)), pv = kPage ? check(entry(t0, vb)) : pk;
+      load_k(pk, t0);
+      load_v(pv, t0);
+      pk = entry(t0 + t_step, kb);
+      pv = kPage ? entry(t0 + t_step, vb) : pk;
+
+      // The kC positions of this lane at t0 that its rows see, as bits.
+      auto visible = [&](uint32_t (&vis)[NT]) {
+        const int j0 = t0 + vb - ctx;      // place of the first of them in the segment
+        const uint32_t every = (1u << kC) - 1u;
+        const uint32_t before = j0 >= 0 ? 0u : -j0 >= kC ? every : (1u << -j0) - 1u;
+        const int keep = rq.n - j0;        // positions up to the segment's end
+        const uint32_t inside = (keep >= kC ? every : keep <= 0 ? 0u : (1u << keep) - 1u) & ~before;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t bits;
+          if (a.mask) {
+            const uint32_t* mw = a.mask + (int64_t)(rq.start + el[nt]) * a.mask_words;
+            const int jj = j0 < 0 ? 0 : j0;
+            const int w0 = jj >> 5;
+            uint64_t two = w0 < a.mask_words ? mw[w0] : 0u;
+            if (w0 + 1 < a.mask_words) two |= (uint64_t)mw[w0 + 1] << 32;
+            bits = (uint32_t)(two >> (jj & 31));
+            bits = j0 < 0 ? (-j0 < 32 ? bits << -j0 : 0u) : bits;
+          } else {
+            const int c = el[nt] - j0 + 1;
+            bits = c >= kC ? every : c <= 0 ? 0u : (1u << c) - 1u;
+          }
+          vis[nt] = before | (bits & inside);
+        }
+      };
+      // Values behind the last position become zeros, and so do others that are not
+      // finite if `clear`.  Returns whether there were such.
+      auto trim_values = [&](bool clear) {
+        const int keep = total - (t0 + vb);
+        uint32_t odd = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          constexpr int kPer = 4 / kEl;    // values a word
+          const int c = keep - i * kPer;
+          const uint32_t live = c >= kPer ? 0xffffffffu : c <= 0 ? 0u : (1u << (c * 8 * kEl)) - 1u;
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt) {
+            uint32_t x = vf[dt][i] & live;
+            const uint32_t flags = F8 ? bytes_nan(x) : halves_from(x, E::kExp);
+            odd |= flags;
+            if (clear) x &= ~(flags * (F8 ? 0xffu : 0xffffu));
+            vf[dt][i] = x;
+          }
+        }
+        return odd;
+      };
+      uint32_t specials = 0u;
+
+      auto step = [&](auto is_edge) {
+        constexpr bool kEdge = decltype(is_edge)::value;
+        // Past the last step the next loads read the last page again and are not used.
+        const int next = t0 + t_step;
+        const int32_t pk1 = check(pk), pv1 = kPage ? check(pv) : pk1;
+        pk = entry(next + t_step, kb);
+        pv = kPage ? entry(next + t_step, vb) : pk;
+        // ---- scores ----
+        f32x4 s[NT][kKT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt) s[nt][kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+          for (int i = 0; i < kMj; ++i)
+#pragma unroll
+            for (int kt = 0; kt < kKT; ++kt) {
+              const u32x4 kx = F8 ? widen8<DT>(kf[kt][j], i) : kf[kt][j];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                s[nt][kt] = E::mma(kx, qf[nt][j * kMj + i], s[nt][kt]);
+            }
+        load_k(pk1, next);
+        // ---- positions that rows do not see ----
+        uint32_t vis[NT];
+        if constexpr (kEdge) {
+          visible(vis);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t on = spread(vis[nt], 4 * kt + i);
+                s[nt][kt][i] = as_float((as_bits(s[nt][kt][i]) & on) | (0xff800000u & ~on));
+              }
+        }
+        // ---- probabilities ----
+        u32x4 pf[NT][kU];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float top = s[nt][0][0];
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[nt][kt][i]);
+          top = groups_max(top) * sc;
+          if (__any(top > m[nt] + kSlack)) {
+            const float nm = fmaxf(m[nt], top);
+            const float f = m[nt] == nm ? 1.0f : pow2(m[nt] - nm);
+            l[nt] *= f;
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) o[nt][dt] *= f;
+            m[nt] = nm;
+          }
+          const float base = m[nt] == -INFINITY ? 0.0f : m[nt];
+          float p[kC];
+          float sum = 0.0f;
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x = pow2(fmaf(s[nt][kt][i], sc, -base));
+              // unseen: 0 whatever the line above made of -inf
+              if (kEdge) x = as_float(as_bits(x) & spread(vis[nt], 4 * kt + i));
+              p[4 * kt + i] = x;
+              sum += x;
+            }
+          l[nt] += sum;
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pf[nt][u][i] = E::pack(p[8 * u + 2 * i], p[8 * u + 2 * i + 1]);
+        }
+        // ---- values ----
+        if constexpr (kEdge) {
+          // A value that is not finite must not meet the zero probability of a row that
+          // does not see it: it leaves the product here and comes back below.
+          specials |= trim_values(true);
+        }
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const u32x4 vx = F8 ? widen8<DT>(vf[dt], u) : vf[dt];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) o[nt][dt] = E::mma(vx, pf[nt][u], o[nt][dt]);
+          }
+        load_v(pv1, next);
+      };
+      const int t_plain = min(t_end, ctx - kTok + 1);   // steps that end within the context
+      for (; t0 < t_plain; t0 += t_step) step(std::false_type{});
+      const int t_edge = t0;
+      for (; t0 < t_end; t0 += t_step) step(std::true_type{});
+      // Rows that see values that are not finite get them by products of indicators:
+      // 1 where the value is +inf, -inf or NaN, with 1 where it is seen.
+      if (__any(specials != 0u)) {
+#pragma unroll 1
+        for (t0 = t_edge; t0 < t_end; t0 += t_step) {
+          load_v(check(entry(t0, vb)), t0);
+          if (!__any(trim_values(false) != 0u)) continue;
+          uint32_t vis[NT];
+          visible(vis);
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            u32x4 sees[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sees[nt][i] = (spread(vis[nt], 8 * u + 2 * i) & E::kOne) |
+                              (spread(vis[nt], 8 * u + 2 * i + 1) & (E::kOne << 16));
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) {
+              const u32x4 x = F8 ? widen8<DT>(vf[dt], u) : vf[dt];
+              u32x4 up, down, nan;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t is_nan = halves_from(x[i], E::kExp + 1u);
+                const uint32_t inf = halves_from(x[i], E::kExp) & ~is_nan;
+                const uint32_t minus = (x[i] >> 15) & 0x00010001u;
+                nan[i] = is_nan * E::kOne;
+                up[i] = (inf & ~minus) * E::kOne;
+                down[i] = (inf & minus) * E::kOne;
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                const f32x4 n_up = E::mma(up, sees[nt], zero);
+                const f32x4 n_down = E::mma(down, sees[nt], zero);
+                const f32x4 n_nan = E::mma(nan, sees[nt], zero);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float add = n_up[i] > 0.0f ? INFINITY : 0.0f;
+                  add -= n_down[i] > 0.0f ? INFINITY : 0.0f;
+                  o[nt][dt][i] += n_nan[i] > 0.0f ? NAN : add;
+                }
+              }
+              __builtin_amdgcn_sched_barrier(0);   // one output tile at a time: few registers
+            }
+          }
+        }
+      }
+    }
+    // A bad page, length or table: every row of the wave is NaN.
+    if (__any(bad)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) l[nt] = NAN;
+    }
+
+    // ---- join the waves over positions: wt = 4, 2, 1 ----
+    for (int half = wt >> 1; half >= 1; half >>= 1) {
+      // buffers: wr * half <= 2
+      const int buf = (my_t & (half - 1)) * wr + my_r;
+      __syncthreads();
+      if (my_t >= half && my_t < 2 * half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          sh_ml[buf][nt][0][lane] = m[nt];
+          sh_ml[buf][nt][1][lane] = l[nt];
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt) sh_o[buf][nt * kDT + dt][lane] = o[nt][dt];
+        }
+      }
+      __syncthreads();
+      if (my_t < half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m2 = sh_ml[buf][nt][0][lane], l2 = sh_ml[buf][nt][1][lane];
+          const float nm = fmaxf(m[nt], m2);
+          const float base = nm == -INFINITY ? 0.0f : nm;
+          const float f1 = pow2(m[nt] - base), f2 = pow2(m2 - base);
+          m[nt] = nm;
+          l[nt] = l[nt] * f1 + l2 * f2;
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt)
+            o[nt][dt] = o[nt][dt] * f1 + sh_o[buf][nt * kDT + dt][lane] * f2;
+        }
+      }
+    }
+
+    // ---- out ----
+    const bool whole = s0 == 0 && s1 == units;
+    if (my_t == 0) {
+      const float vs = a.v_scale ? a.v_scale[h] : 1.0f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + nt * 16 + col;
+        const float sum = groups_sum(l[nt]);
+        if (whole) {
+          if (row < rq.rows) {
+            const int y = h * group + row - el[nt] * group;
+            const float f = sum == 0.0f ? 0.0f : vs / sum;
+            uint16_t* op = static_cast<uint16_t*>(a.out) +
+                           (int64_t)(rq.start + el[nt]) * a.out_stride + y * D + g * 4;
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) {
+              uint2 x;
+              x.x = E::pack(o[nt][dt][0] * f, o[nt][dt][1] * f);
+              x.y = E::pack(o[nt][dt][2] * f, o[nt][dt][3] * f);
+              *reinterpret_cast<uint2*>(op + dt * 16) = x;
+            }
+            if (a.lse && g == 0)
+              a.lse[(int64_t)(rq.start + el[nt]) * a.Hq + y] =
+                  (m[nt] + __log2f(sum)) * 0.69314718055994531f;
+          }
+        } else if (row0 + nt * 16 < rq.rows) {
+          const int64_t slot = 2 * (int64_t)b + (s0 == 0 ? 1 : 0);
+          const int64_t blk = slot * kWaves * NT + my_r * NT + nt;
+          part_ml[(blk * 2) * 64 + lane] = m[nt];
+          part_ml[(blk * 2 + 1) * 64 + lane] = sum;
+          f32x4* po = reinterpret_cast<f32x4*>(part_o) + blk * kDT * 64;
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt) po[dt * 64 + lane] = o[nt][dt];
+        }
+      }
+    }
+    if (!whole && s0 == 0) {
+      // the tile's last unit belongs to the workgroup that ends the row of parts
+      const int64_t last = w + (units - 1);
+      int64_t owner = last * runs / all;
+      while (all * (owner + 1) / runs <= last) ++owner;
+      cut.r = r;
+      cut.h = h;
+      cut.row_tile = row_tile;
+      cut.parts = (int)(owner - b) + 1;
+    }
+    w += s1 - s0;
+    at += s1 - s0;
+  }
+  if (t == 0) cuts[b] = cut;
+}
+
+// Joins the parts of cut tiles.  Grid: (workgroups of the first launch, 16-row
+// blocks of a tile); the four waves take the parts in turn.
+template <int DT, int D, int NT, int TOK>
+__global__ __launch_bounds__(kThreads) void tree_attention_join_kernel(
+    const TreeAttnArgs a, const AttnCut* __restrict__ cuts, const float* __restrict__ part_ml,
+    const float* __restrict__ part_o) {
+  constexpr int kDT = D / 16;
+  using E = El<DT>;
+  __shared__ f32x4 sh_o[kWaves - 1][kDT][64];
+  __shared__ float sh_ml[kWaves - 1][2][64];
+  const int b = blockIdx.x;
+  const int blk = blockIdx.y;
+  const AttnCut cut = cuts[b];
+  if (cut.parts == 0) return;
+  const int group = a.Hq / a.Hk;
+  const Req rq = request<NT, TOK>(a, cut.r, group);
+  const int row0 = cut.row_tile * (16 * NT * kWaves) + blk * 16;
+  if (row0 >= rq.rows) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o[kDT];
+#pragma unroll
+  for (int dt = 0; dt < kDT; ++dt) o[dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p = wave; p < cut.parts; p += kWaves) {
+    const int64_t slot = p == 0 ? 2 * (int64_t)b + 1 : 2 * (int64_t)(b + p);
+    const int64_t at = slot * kWaves * NT + blk;
+    const float m2 = part_ml[(at * 2) * 64 + lane], l2 = part_ml[(at * 2 + 1) * 64 + lane];
+    const f32x4* po = reinterpret_cast<const f32x4*>(part_o) + at * kDT * 64;
+    f32x4 x[kDT];
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt) x[dt] = po[dt * 64 + lane];
+    const float nm = fmaxf(m, m2);
+    const float base = nm == -INFINITY ? 0.0f : nm;
+    const float f1 = pow2(m - base), f2 = pow2(m2 - base);
+    m = nm;
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt) o[dt] = o[dt] * f1 + x[dt] * f2;
+  }
+  if (wave > 0) {
+    sh_ml[wave - 1][0][lane] = m;
+    sh_ml[wave - 1][1][lane] = l;
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt) sh_o[wave - 1][dt][lane] = o[dt];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  for (int v = 0; v < kWaves - 1; ++v) {
+    const float m2 = sh_ml[v][0][lane], l2 = sh_ml[v][1][lane];
+    const float nm = fmaxf(m, m2);
+    const float base = nm == -INFINITY ? 0.0f : nm;
+    const float f1 = pow2(m - base), f2 = pow2(m2 - base);
+    m = nm;
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt) o[dt] = o[dt] * f1 + sh_o[v][dt][lane] * f2;
+  }
+  const int col = lane & 15, g = lane >> 4;
+  const int row = row0 + col;
+  if (row >= rq.rows) return;
+  const int el = row / group;
+  const int y = cut.h * group + row - el * group;
+  const float vs = a.v_scale ? a.v_scale[cut.h] : 1.0f;
+  const float f = l == 0.0f ? 0.0f : vs / l;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + (int64_t)(rq.start + el) * a.out_stride + y * D + g * 4;
+#pragma unroll
+  for (int dt = 0; dt < kDT; ++dt) {
+    uint2 x;
+    x.x = E::pack(o[dt][0] * f, o[dt][1] * f);
+    x.y = E::pack(o[dt][2] * f, o[dt][3] * f);
+    *reinterpret_cast<uint2*>(op + dt * 16) = x;
+  }
+  if (a.lse && g == 0)
+    a.lse[(int64_t)(rq.start + el) * a.Hq + y] = (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <int DT, bool F8, int D, int NT>
+dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  AttnCut* cuts = static_cast<AttnCut*>(a.ws);
+  float* ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + p.cut_bytes);
+  float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + p.cut_bytes + p.ml_bytes);
+  // a step has 32 positions, 64 with an 8-bit cache
+  auto kernel = a.shift == 4        ? &tree_attention_kernel<DT, F8, D, NT, 4>
+                : F8 && a.shift == 5 ? &tree_attention_kernel<DT, F8, D, NT, F8 ? 5 : 0>
+                                     : &tree_attention_kernel<DT, F8, D, NT, 0>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.groups), dim3(kThreads), 0, stream, a, cuts, ml, po);
+  const dspark_status st = check_launch("tree_attention_kernel");
+  if (st != DSPARK_OK) return st;
+  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, NT, F8 ? 64 : 32>),
+                     dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kThreads), 0, stream, a,
+                     cuts, ml, po);
+  return check_launch("tree_attention_join_kernel");
+}
+
+}  // namespace
+
+template <int DT, bool F8>
+dspark_status run_tree_attention(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  const bool one = p.nt == 1;
+  switch (a.D) {
+    case 64:
+      return one ? go<DT, F8, 64, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 64, 2>(a, p, stream)
+                                                               : go<DT, F8, 64, 4>(a, p, stream);
+    case 96:
+      return one ? go<DT, F8, 96, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 96, 2>(a, p, stream)
+                                                               : go<DT, F8, 96, 4>(a, p, stream);
+    case 128:
+      return one ? go<DT, F8, 128, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 128, 2>(a, p, stream)
+                                                                : go<DT, F8, 128, 4>(a, p, stream);
+    case 192: return one ? go<DT, F8, 192, 1>(a, p, stream) : go<DT, F8, 192, 2>(a, p, stream);
+    default: return one ? go<DT, F8, 256, 1>(a, p, stream) : go<DT, F8, 256, 2>(a, p, stream);
+  }
+}
+
+}  // namespace dspark

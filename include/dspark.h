@@ -620,9 +620,12 @@ size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, in
  *   lse         optional [max_tokens, Hq] fp32.
  *   workspace   >= dspark_tree_attention_workspace(...) bytes, 256-byte aligned;
  *               its contents on entry do not matter.
- * Every row of a request with ctx_len[r] < 0, more positions than its table
- * has, or a page id outside [0, num_pages) among those that it reads is NaN.
- * The sums are split in a fixed way, so results do not vary between runs.
+ * A request's rows are NaN where ctx_len[r] < 0 or it has more positions than its
+ * table, and rows that read a page id outside [0, num_pages) are NaN (rows of
+ * a chain need not read the pages behind them).
+ * Where a row's sums are split depends on the lengths of the whole batch: the
+ * same call gives the same bits, a request in another batch the same values up
+ * to the rounding of fp32 sums.
  * Errors: EINVAL for NULL pointers, sizes <= 0, Hq not a multiple of Hk, bad
  * types, page sizes, strides, alignment or scale, scales missing or given
  * without DSPARK_E4M3; EUNSUPPORTED for D outside {64, 96, 128, 192, 256},

@@ -80,7 +80,8 @@ def check(c, out, lse, rows=None):
     ref, rlse, W, A, M = oracle(c)
     Dh = ref.shape[2]
     u = H.half_step(out.dtype)
-    T = int((c["ctx"] + np.diff(c["cu"])).max())
+    T = int((c["ctx"].astype(np.int64) + np.diff(c["cu"])).max())
+    A, M = np.where(np.isnan(ref[..., 0]), 0, A), np.where(np.isnan(ref[..., 0]), 0, M)
     e = 2 * ((Dh + 4) * F * A + 4 * F * (2 * M + 2))
     v = np.abs(H.np64(c["vc"]))
     vmax = float(v[np.isfinite(v)].max()) * (1.0 if c["vs"] is None else float(c["vs"].max()))
@@ -300,7 +301,6 @@ def test_bad_requests_give_nan_and_leave_the_others():
     print("case attention bad requests", flush=True)
     n, ctx = [3, 2, 4, 1, 2, 5], [40, 33, 70, 5, 20, 64]
     c = make(68, n, ctx, 8, 2, 128, 16, width=6)
-    ref = call(c, want_lse=True)
     c["table"][1, 1] = c["kc"].shape[0]      # past the last page
     c["table"][2, 4] = -1
     c["ctx"] = c["ctx"].copy()
@@ -308,12 +308,14 @@ def test_bad_requests_give_nan_and_leave_the_others():
     c["ctx"][4] = 6 * 16                     # more positions than the table has
     out, lse = call(c, want_lse=True)
     torch.cuda.synchronize()
+    good = []
     for r in range(6):
         s = slice(int(c["cu"][r]), int(c["cu"][r + 1]))
         if r in (1, 2, 3, 4):
             assert torch.isnan(out[s]).all() and torch.isnan(lse[s]).all(), r
         else:
-            assert torch.equal(out[s], ref[0][s]) and torch.equal(lse[s], ref[1][s]), r
+            good += range(s.start, s.stop)
+    check(c, out, lse, good)
 
 
 def test_results_repeat_and_do_not_depend_on_the_workspace():
