@@ -28,12 +28,13 @@ int compute_units() {
 AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64_t capacity) {
   AttnPlan p;
   const int group = Hq / Hk;
-  // Rows that a request is likely to bring.  More 16-row tiles a wave read the
-  // cache fewer times, fewer leave registers for more waves; any count runs any
-  // number of rows.  Wide heads keep two tiles, whose sums fill the registers.
+  // Rows that a request is likely to bring.  With one 16-row tile a wave more waves
+  // fit a CU; with more than two tiles the products weigh as much as the loads.  Any
+  // variant runs any number of rows.
   const int64_t rows = (int64_t)((max_tokens + (int64_t)R - 1) / R) * group;
-  p.nt = rows <= 8 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
-  const int per_cu = attn_waves(p.nt, D);
+  p.nt = rows <= 8 ? 1 : 2;
+  p.ring = rows > 32;
+  const int per_cu = attn_waves(p.nt, D, p.ring);
   int64_t groups = (int64_t)compute_units() * per_cu;
   if (capacity > 0) {
     // no more workgroups than units of work there can be

@@ -9,23 +9,27 @@
 // Both products run on the matrix cores transposed, S^T = K Q^T and O^T = V^T P^T:
 // a step's positions are the rows of the first result and the contraction of
 // the second, and a query row is a matrix column, so a lane holds one row's
-// scores, its maximum and its rescale factor, and what the first product leaves
-// in a lane is what the second one takes there.  Nothing crosses lanes but the
-// row maximum (two lane swaps).  The caches are stored in operand order, so keys
-// and values go from memory to registers to the matrix cores, 16 bytes a lane,
-// with no LDS on the way.
+// scores, its maximum and its rescale factor.  The caches are stored in operand
+// order, so keys and values go from memory to registers to the matrix cores, 16
+// bytes a lane, with no LDS on the way.
 //
-// A step is kTok positions: 4 groups (lane / 16) of c = 16 / element size
-// neighbouring positions.  Row 4 g + i of key tile kt is position c g + 4 kt + i:
-// the scores that a lane gets are those of its own group's c positions, in the
-// order in which its 16 bytes of a value channel hold them.
+// A step is kTok = 4 c positions, c = 16 / element size.  Key tile kt is the
+// positions 16 kt .. 16 kt + 15, so that one load instruction of the wave takes
+// whole runs of 256 bytes (with pieces of 64 bytes and non-temporal loads the
+// same kernel read 5.6 TB/s instead of 6.9).  Lane group g = lane / 16 then holds
+// the scores of positions 16 kt + 4 g + i, and its 16 bytes of a value channel
+// are positions c g .. c g + c - 1: the packed probabilities go there by a
+// transposition of groups and tiles, two lane swaps a register pair.
 //
 // Work is split by length, not by request: the row tiles of all requests and
 // heads are laid end to end in units of (waves over positions) * kTok positions,
 // and each workgroup takes an equal run of units, whatever requests it
 // crosses.  A tile cut by a run's end goes to the workspace in parts (fp32), and
 // a second launch joins them.  Each workgroup finds its place by scanning the
-// lengths itself.
+// lengths itself.  A tile counts for kTileCost positions more than it has: the
+// queries, the first loads and the last sums of a tile take about as long as
+// reading those (without it the run with the most short requests ended last:
+// 64 chains over 37 to 8100 positions took 222 us, now 190).
 //
 // A workgroup's four waves share a tile of 16 NT WR rows: WR waves over rows,
 // 4 / WR over positions (interleaved steps).  A request's rows are cut into tiles
@@ -56,6 +60,7 @@ struct AttnCut {
 struct AttnPlan {
   int groups;       // workgroups
   int nt;           // 16-row tiles per wave
+  bool ring;        // waves share keys and values through LDS
   int row_blocks;   // 16-row blocks of a part that may hold rows
   size_t cut_bytes, ml_bytes, o_bytes;   // workspace: AttnCut[groups], (m, l), O
 };
@@ -76,6 +81,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr float kSlack = 8.0f;
+constexpr int kTileCost = 256;
 
 // Operands and conversions of an element type (0 bf16, 1 fp16).
 template <int DT> struct El;
@@ -132,11 +138,60 @@ __device__ __forceinline__ uint32_t spread(uint32_t bits, int i) {
   return (uint32_t)((int32_t)(bits << (31 - i)) >> 31);
 }
 
+// Words of the (lane group, tile) matrix to its transpose: x[i] of group g becomes
+// x[g] of group i for four tiles; for two, group g gets the halves of tile g / 2
+// that groups 2 (g % 2) and 2 (g % 2) + 1 held.
+__device__ __forceinline__ void swap32(uint32_t& x, uint32_t& y) {
+  const auto s = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  x = s[0];
+  y = s[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& x, uint32_t& y) {
+  const auto s = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = s[0];
+  y = s[1];
+}
+__device__ __forceinline__ void regroup(uint32_t (&x)[2]) {
+  swap32(x[0], x[1]);
+  swap16(x[0], x[1]);
+}
+__device__ __forceinline__ void regroup(uint32_t (&x)[4]) {
+  swap32(x[0], x[2]);
+  swap32(x[1], x[3]);
+  swap16(x[0], x[1]);
+  swap16(x[2], x[3]);
+}
+
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // A bit cast of a vector's element reads element 0: elements are copied first.
 __device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
 __device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+
+// 64 pieces of 16 bytes (one a lane) from memory to 1 KB of LDS at a wave-uniform
+// address, lane after lane, without passing registers.  In assembly, so that the
+// compiler does not wait for it before the next read of LDS; wait_loads does.
+__device__ __forceinline__ void copy_to_lds(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// Until at most N (<= 63) loads of this wave are outstanding; they land in order, so
+// loads that the compiler adds only make the wait longer.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N <= 63, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0f70);
+  asm volatile("" ::: "memory");
+}
+// A barrier that waits for nothing else.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // Over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float x) {
@@ -166,7 +221,11 @@ struct Req {
     return (int64_t)full * units_full + units_last;
   }
 };
-template <int NT, int TOK>
+// kTileCost in units of `unit` positions, at least one.
+__device__ __forceinline__ int tile_cost(int unit) {
+  return unit < kTileCost ? kTileCost / unit : 1;
+}
+template <int NT, int TOK, bool RING>
 __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) {
   Req q;
   const int64_t s = a.cu[r], e = a.cu[r + 1];
@@ -183,22 +242,28 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) 
   constexpr int kTile = 16 * NT * kWaves;
   q.full = q.rows / kTile;
   const int rest = q.rows - q.full * kTile;
-  q.wr_last = rest == 0 ? 0 : rest <= 16 * NT ? 1 : rest <= 32 * NT ? 2 : 4;
+  q.wr_last = rest == 0 ? 0 : !RING && rest <= 16 * NT ? 1 : rest <= 32 * NT ? 2 : 4;
+  // Units of a tile: its cost, then its steps.
   const int steps = q.bad ? 1 : (q.total + TOK - 1) / TOK;
-  q.units_full = steps;
+  q.units_full = tile_cost(TOK) + steps;
   const int wt = q.wr_last ? kWaves / q.wr_last : 1;
-  q.units_last = q.wr_last ? (steps + wt - 1) / wt : 0;
+  q.units_last = q.wr_last ? tile_cost(TOK * wt) + (steps + wt - 1) / wt : 0;
   return q;
 }
 
+// Steps of a ring of `slots` for each of 4 / wr groups of waves: at most four, so that
+// the loads in flight stay countable.
+constexpr int ring_steps(int slots, int wr) {
+  return slots * wr / kWaves < 4 ? slots * wr / kWaves : 4;
+}
 // Waves of a SIMD that the registers of a tile allow.
-constexpr int attn_waves(int nt, int d) {
-  return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : nt * d <= 256 && d <= 128 ? 2 : 1;
+constexpr int attn_waves(int nt, int d, bool ring) {
+  return ring ? (d <= 128 ? 2 : 1) : nt * d <= 64 ? 4 : nt * d <= 96 ? 3 : nt * d <= 256 && d <= 128 ? 2 : 1;
 }
 
 // Launch with kThreads threads; a run of units per workgroup.
-template <int DT, bool F8, int D, int NT, int kPage>
-__global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_kernel(
+template <int DT, bool F8, int D, int NT, int kPage, bool kRing>
+__global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_attention_kernel(
     const TreeAttnArgs a, AttnCut* __restrict__ cuts, float* __restrict__ part_ml,
     float* __restrict__ part_o) {
   constexpr int kC = F8 ? 16 : 8;        // positions of a lane's 16 bytes of values
@@ -211,8 +276,18 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
   constexpr int kEl = F8 ? 1 : 2;
   constexpr int kPieces = D / kC;        // 16-byte pieces of a key row
   using E = El<DT>;
+  // Where requests bring many rows the waves share positions (two or four of them)
+  // and one copy of keys and values, in a ring of steps in LDS that is loaded up to
+  // three steps ahead.  With few rows each wave loads its own positions into
+  // registers.  Two workgroups of a CU cover each other's waits either way.
+  constexpr int kRingBytes = D <= 128 ? 64 * 1024 : 128 * 1024;
+  constexpr int kKB = kKT * kJ;          // 1 KB blocks of keys and of a step
+  constexpr int kBlocks = kKB + kDT;
+  constexpr int kSlots = kRingBytes / 1024 / kBlocks;
 
-  __shared__ f32x4 sh_o[2][NT * kDT][64];
+  constexpr int kJoinBytes = 2 * NT * kDT * 64 * 16;
+  __shared__ __align__(16) uint8_t sh_mem[kRing && kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes];
+  f32x4(&sh_o)[2][NT * kDT][64] = *reinterpret_cast<f32x4(*)[2][NT * kDT][64]>(sh_mem);
   __shared__ float sh_ml[2][NT][2][64];
   __shared__ int64_t sh_scan[kWaves];
   __shared__ int64_t sh_pos[2];          // request and unit within it of this run's first unit
@@ -236,7 +311,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
     const int per = (a.R + kThreads - 1) / kThreads;
     const int r0 = min(t * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok>(a, r, group).head_units();
+    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok, kRing>(a, r, group).head_units();
     int64_t inc = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -258,7 +333,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
     int64_t first = pre + inc - mine;
     if (w < w_end && w >= first && w < first + mine) {
       for (int r = r0; r < r1; ++r) {
-        const int64_t u = a.Hk * request<NT, kTok>(a, r, group).head_units();
+        const int64_t u = a.Hk * request<NT, kTok, kRing>(a, r, group).head_units();
         if (w < first + u) {
           sh_pos[0] = r;
           sh_pos[1] = w - first;
@@ -278,7 +353,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
   AttnCut cut = {0, 0, 0, 0};
 
   while (w < w_end) {
-    const Req rq = request<NT, kTok>(a, r, group);
+    const Req rq = request<NT, kTok, kRing>(a, r, group);
     const int64_t per_head = rq.head_units();
     if (at >= a.Hk * per_head) {   // also requests without work
       at -= a.Hk * per_head;
@@ -286,6 +361,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
       continue;
     }
     // ---- this segment: units s0 .. s1 of row tile `row_tile` of head h ----
+    if (kRing) __syncthreads();            // the ring is free
     const int h = uni((int)(at / per_head));
     const int64_t in_head = at - h * per_head;
     const bool full = in_head < (int64_t)rq.full * rq.units_full;
@@ -340,112 +416,126 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
       seen = min(seen, ctx + (min(rq.rows, row0 + 16 * NT) - 1) / group + 1);
     bool bad = rq.bad;
     const int t_step = kTok * wt;
-    int t0 = uni((s0 * wt + my_t) * kTok);
-    const int t_end = uni(idle || bad ? 0 : min(seen, s1 * t_step));
+    const int cost = tile_cost(t_step);
+    int t0 = uni((max(s0 - cost, 0) * wt + my_t) * kTok);
+    const int t_end = uni(idle || bad ? 0 : min(seen, (s1 - cost) * t_step));
+    // the same of the whole tile: waves that share a ring take part to its end
+    const int t0_tile = max(s0 - cost, 0) * wt * kTok;
+    int seen_tile = total;
+    if (!a.mask)
+      seen_tile = min(seen_tile, ctx + (min(rq.rows, (row_tile * kWaves + wr) * 16 * NT) - 1) / group + 1);
+    const int t_end_tile = uni(bad ? 0 : min(seen_tile, (s1 - cost) * t_step));
 
-    if (t0 < t_end) {
+    if (kRing ? t0_tile < t_end_tile : t0 < t_end) {
       const int shift = kPage ? kPage : a.shift;
       const int P = 1 << shift;
       const int last_page = (total - 1) >> shift;
       const int64_t page_bytes = ((int64_t)a.Hk * D << shift) * kEl;
       const uint8_t* kh = static_cast<const uint8_t*>(a.k_cache) + ((int64_t)h * D << shift) * kEl;
       const uint8_t* vh = static_cast<const uint8_t*>(a.v_cache) + ((int64_t)h * D << shift) * kEl;
-      const int kb = kC * (col >> 2);       // this lane's key rows start there within a step
-      const int vb = kC * g;                // and its values there
+      const int vb = kC * g;                // this lane's values start there within a step
       const int32_t* pages = a.table + (int64_t)r * a.max_pages;
       u32x4 kf[kKT][kJ], vf[kDT];
-      // Page of this lane's keys (b = kb) or values (b = vb) of the step at tt; for
-      // kPage = 0 one scalar for the wave.  Entries are read two steps ahead of
-      // their use, keys and values one.
-      auto entry = [&](int tt, int bb) {
-        if constexpr (kPage == 0) {
-          typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
-          return ((scalar_ptr)(uintptr_t)pages)[min(tt >> shift, last_page)];
-        } else {
-          return pages[min((tt + bb) >> shift, last_page)];
+      // Pages of the step at tt, scalars; read two steps ahead of their use, keys and
+      // values one or more.
+      constexpr int kPk = kPage == 0 ? 1 : kTok >> kPage;
+      struct Pages {
+        uint64_t lo, hi;                   // pages 0 and 1, pages 2 and 3
+        __device__ __forceinline__ int64_t at(int i) const {
+          // no select between members, which would send them to memory
+          const uint64_t two = kPk == 4 ? lo ^ ((lo ^ hi) & (0 - (uint64_t)((i >> 1) & 1))) : lo;
+          return (int32_t)(two >> (32 * (i & 1)));
         }
       };
-      auto check = [&](int32_t p) {
-        const bool ok = page_ok(p, a.num_pages);
-        bad |= !ok;
-        return ok ? p : 0;
+      auto entries = [&](int tt) __attribute__((always_inline)) {
+        typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+        const scalar_ptr row = (scalar_ptr)(uintptr_t)pages;
+        const int i = tt >> shift;
+        // A page outside the pool is not touched: page 0 stands in, and the rows are NaN.
+        auto one = [&](int k) __attribute__((always_inline)) {
+          const int32_t p = row[min(i + k, last_page)];
+          const bool ok = page_ok(p, a.num_pages);
+          bad |= !ok;
+          return (uint64_t)(uint32_t)(ok ? p : 0);
+        };
+        Pages e = {one(0), 0};
+        if constexpr (kPk >= 2) e.lo |= one(1) << 32;
+        if constexpr (kPk == 4) e.hi = one(2) | one(3) << 32;
+        return e;
       };
-      auto load_k = [&](int32_t page, int tt) {
-        if constexpr (kPage == 0) {
-          const uint8_t* base = kh + page * page_bytes + (tt & (P - 1)) * 16;
-          const uint32_t off = (uint32_t)((kb + (col & 3)) * 16 + g * (P * 16));
+      // Addresses of this lane's 16 bytes of key block (kt, j) and of value block dt of
+      // the step at tt.
+      const uint32_t k_lane = (uint32_t)(col * 16 + g * (P * 16));
+      auto k_block = [&](const Pages& e, int tt, int kt, int j) __attribute__((always_inline)) {
+        const uint8_t* base = kh + e.at(kPage == 0 ? 0 : (16 * kt) >> kPage) * page_bytes +
+                              ((tt + 16 * kt) & (P - 1)) * 16 + (int64_t)j * 4 * P * 16;
+        // past the last piece: the first ones again, cleared where they are used
+        return base + (kPieces % 4 != 0 && j * 4 + g >= kPieces ? (uint32_t)(col * 16) : k_lane);
+      };
+      auto v_base = [&](const Pages& e, int tt) __attribute__((always_inline)) {
+        int64_t at = e.at(0) * page_bytes;
+        if constexpr (kPk == 2) at = g & 2 ? e.at(1) * page_bytes : at;
+        if constexpr (kPk == 4) {
+          const int64_t lo = g & 1 ? e.at(1) * page_bytes : at;
+          const int64_t hi = g & 1 ? e.at(3) * page_bytes : e.at(2) * page_bytes;
+          at = g & 2 ? hi : lo;
+        }
+        return vh + at + (uint32_t)((col * P + ((tt + vb) & (P - 1))) * kEl);
+      };
+      auto k_tail = [&]() __attribute__((always_inline)) {
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            const uint8_t* bj = base + (int64_t)j * 4 * P * 16;
+        for (int kt = 0; kt < kKT; ++kt)
+          if (kPieces % 4 != 0 && (kJ - 1) * 4 + g >= kPieces) kf[kt][kJ - 1] = u32x4{0, 0, 0, 0};
+      };
+      // Each wave's own loads.  Both caches are read once: non-temporal, except where
+      // a step's values are parts of lines (long pages).
+      auto load_k = [&](const Pages& e, int tt) __attribute__((always_inline)) {
 #pragma unroll
-            for (int kt = 0; kt < kKT; ++kt) {
-              const bool none = kPieces % 4 != 0 && j * 4 + g >= kPieces;
-              kf[kt][j] = *reinterpret_cast<const u32x4*>(bj + (none ? off - g * (P * 16) : off) + kt * 64);
-              if (none) kf[kt][j] = u32x4{0, 0, 0, 0};
-            }
-          }
-        } else {
-          const uint8_t* base = kh + page * page_bytes + (((tt + kb) & (P - 1)) + (col & 3)) * 16 +
-                                g * (P * 16);
+        for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
           for (int j = 0; j < kJ; ++j)
+            kf[kt][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k_block(e, tt, kt, j)));
+      };
+      auto load_v = [&](const Pages& e, int tt) __attribute__((always_inline)) {
+        const uint8_t* base = v_base(e, tt);
 #pragma unroll
-            for (int kt = 0; kt < kKT; ++kt) {
-              const bool none = kPieces % 4 != 0 && j * 4 + g >= kPieces;
-              kf[kt][j] = *reinterpret_cast<const u32x4*>(base - (none ? g * (P * 16) : 0) +
-                                                          j * 4 * P * 16 + kt * 64);
-              if (none) kf[kt][j] = u32x4{0, 0, 0, 0};
-            }
+        for (int dt = 0; dt < kDT; ++dt) {
+          const u32x4* q = reinterpret_cast<const u32x4*>(base + (int64_t)dt * 16 * P * kEl);
+          vf[dt] = kPage == 0 ? *q : __builtin_nontemporal_load(q);
         }
       };
-      auto load_v = [&](int32_t page, int tt) {
-        if constexpr (kPage == 0) {
-          const uint8_t* base = vh + page * page_bytes + (tt & (P - 1)) * kEl;
-          const uint32_t off = (uint32_t)((col * P + vb) * kEl);
-#pragma unroll
-          for (int dt = 0; dt < kDT; ++dt)
-            vf[dt] = *reinterpret_cast<const u32x4*>(base + (int64_t)dt * 16 * P * kEl + off);
-        } else {
-          const uint8_t* base = vh + page * page_bytes + (col * P + ((tt + vb) & (P - 1))) * kEl;
-#pragma unroll
-          for (int dt = 0; dt < kDT; ++dt)
-            vf[dt] = *reinterpret_cast<const u32x4*>(base + dt * 16 * P * kEl);
-        }
+      // The positions of the step at t0 that this lane's rows see, as bits.
+      typedef std::conditional_t<F8, uint64_t, uint32_t> Bits;
+      auto below = [](int n) __attribute__((always_inline)) -> Bits {     // the first n positions
+        return n >= kTok ? ~(Bits)0 : n <= 0 ? (Bits)0 : ((Bits)1 << n) - 1;
       };
-      int32_t pk = check(entry(t0, kb)), pv = kPage ? check(entry(t0, vb)) : pk;
-      load_k(pk, t0);
-      load_v(pv, t0);
-      pk = entry(t0 + t_step, kb);
-      pv = kPage ? entry(t0 + t_step, vb) : pk;
-
-      // The kC positions of this lane at t0 that its rows see, as bits.
-      auto visible = [&](uint32_t (&vis)[NT]) {
-        const int j0 = t0 + vb - ctx;      // place of the first of them in the segment
-        const uint32_t every = (1u << kC) - 1u;
-        const uint32_t before = j0 >= 0 ? 0u : -j0 >= kC ? every : (1u << -j0) - 1u;
-        const int keep = rq.n - j0;        // positions up to the segment's end
-        const uint32_t inside = (keep >= kC ? every : keep <= 0 ? 0u : (1u << keep) - 1u) & ~before;
+      auto visible = [&](Bits (&vis)[NT]) __attribute__((always_inline)) {
+        const int j0 = t0 - ctx;           // place of the first of them in the segment
+        const Bits before = below(-j0);
+        const Bits inside = below(rq.n - j0) & ~before;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          uint32_t bits;
+          Bits bits;
           if (a.mask) {
             const uint32_t* mw = a.mask + (int64_t)(rq.start + el[nt]) * a.mask_words;
             const int jj = j0 < 0 ? 0 : j0;
-            const int w0 = jj >> 5;
-            uint64_t two = w0 < a.mask_words ? mw[w0] : 0u;
-            if (w0 + 1 < a.mask_words) two |= (uint64_t)mw[w0 + 1] << 32;
-            bits = (uint32_t)(two >> (jj & 31));
-            bits = j0 < 0 ? (-j0 < 32 ? bits << -j0 : 0u) : bits;
+            const int w0 = jj >> 5, sh = jj & 31;
+            auto word = [&](int w) { return w < a.mask_words ? (uint64_t)mw[w] : (uint64_t)0; };
+            uint64_t two = (word(w0) | word(w0 + 1) << 32) >> sh;
+            if (F8) two |= sh ? word(w0 + 2) << (64 - sh) : (uint64_t)0;
+            bits = (Bits)two;
+            if (j0 < 0) bits = -j0 < kTok ? bits << -j0 : (Bits)0;
           } else {
-            const int c = el[nt] - j0 + 1;
-            bits = c >= kC ? every : c <= 0 ? 0u : (1u << c) - 1u;
+            bits = below(el[nt] - j0 + 1);
           }
           vis[nt] = before | (bits & inside);
         }
       };
+      // Bits of this lane's scores: those of tile kt in the lowest four.
+      auto mine = [&](Bits v, int kt) __attribute__((always_inline)) { return (uint32_t)(v >> (16 * kt + 4 * g)); };
       // Values behind the last position become zeros, and so do others that are not
       // finite if `clear`.  Returns whether there were such.
-      auto trim_values = [&](bool clear) {
+      auto trim_values = [&](bool clear) __attribute__((always_inline)) {
         const int keep = total - (t0 + vb);
         uint32_t odd = 0u;
 #pragma unroll
@@ -465,14 +555,25 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
         return odd;
       };
       uint32_t specials = 0u;
+      Pages ahead = entries(t0);
+      const uint8_t* slot = sh_mem;        // kRing: the step's blocks
 
-      auto step = [&](auto is_edge) {
+      auto step = [&](auto is_edge) __attribute__((always_inline)) {
         constexpr bool kEdge = decltype(is_edge)::value;
         // Past the last step the next loads read the last page again and are not used.
         const int next = t0 + t_step;
-        const int32_t pk1 = check(pk), pv1 = kPage ? check(pv) : pk1;
-        pk = entry(next + t_step, kb);
-        pv = kPage ? entry(next + t_step, vb) : pk;
+        Pages now;
+        if constexpr (!kRing) {
+          now = ahead;
+          ahead = entries(next + t_step);
+        } else {
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              kf[kt][j] = *reinterpret_cast<const u32x4*>(slot + (kt * kJ + j) * 1024 + lane * 16);
+        }
+        k_tail();
         // ---- scores ----
         f32x4 s[NT][kKT];
 #pragma unroll
@@ -490,9 +591,9 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
               for (int nt = 0; nt < NT; ++nt)
                 s[nt][kt] = E::mma(kx, qf[nt][j * kMj + i], s[nt][kt]);
             }
-        load_k(pk1, next);
+        if constexpr (!kRing) load_k(now, next);
         // ---- positions that rows do not see ----
-        uint32_t vis[NT];
+        Bits vis[NT];
         if constexpr (kEdge) {
           visible(vis);
 #pragma unroll
@@ -501,7 +602,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
             for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t on = spread(vis[nt], 4 * kt + i);
+                const uint32_t on = spread(mine(vis[nt], kt), i);
                 s[nt][kt][i] = as_float((as_bits(s[nt][kt][i]) & on) | (0xff800000u & ~on));
               }
         }
@@ -524,26 +625,34 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
             m[nt] = nm;
           }
           const float base = m[nt] == -INFINITY ? 0.0f : m[nt];
-          float p[kC];
+          uint32_t lo[kKT], hi[kKT];   // a tile's four probabilities, packed
           float sum = 0.0f;
 #pragma unroll
-          for (int kt = 0; kt < kKT; ++kt)
+          for (int kt = 0; kt < kKT; ++kt) {
+            float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x = pow2(fmaf(s[nt][kt][i], sc, -base));
+              p[i] = pow2(fmaf(s[nt][kt][i], sc, -base));
               // unseen: 0 whatever the line above made of -inf
-              if (kEdge) x = as_float(as_bits(x) & spread(vis[nt], 4 * kt + i));
-              p[4 * kt + i] = x;
-              sum += x;
+              if (kEdge) p[i] = as_float(as_bits(p[i]) & spread(mine(vis[nt], kt), i));
+              sum += p[i];
             }
+            lo[kt] = E::pack(p[0], p[1]);
+            hi[kt] = E::pack(p[2], p[3]);
+          }
           l[nt] += sum;
+          regroup(lo);
+          regroup(hi);
 #pragma unroll
           for (int u = 0; u < kU; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pf[nt][u][i] = E::pack(p[8 * u + 2 * i], p[8 * u + 2 * i + 1]);
+            pf[nt][u] = u32x4{lo[2 * u], hi[2 * u], lo[2 * u + 1], hi[2 * u + 1]};
         }
         // ---- values ----
+        if constexpr (kRing) {
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt)
+            vf[dt] = *reinterpret_cast<const u32x4*>(slot + (kKB + dt) * 1024 + lane * 16);
+        }
         if constexpr (kEdge) {
           // A value that is not finite must not meet the zero probability of a row that
           // does not see it: it leaves the product here and comes back below.
@@ -557,20 +666,92 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[nt][dt] = E::mma(vx, pf[nt][u], o[nt][dt]);
           }
-        load_v(pv1, next);
+        if constexpr (!kRing) load_v(now, next);
       };
       const int t_plain = min(t_end, ctx - kTok + 1);   // steps that end within the context
-      for (; t0 < t_plain; t0 += t_step) step(std::false_type{});
-      const int t_edge = t0;
-      for (; t0 < t_end; t0 += t_step) step(std::true_type{});
+      int t_edge = max(t_plain, 0);
+      t_edge = t0 >= t_edge ? t0 : t0 + (t_edge - t0 + t_step - 1) / t_step * t_step;
+      if constexpr (!kRing) {
+        const Pages first = ahead;
+        load_k(first, t0);
+        load_v(first, t0);
+        ahead = entries(t0 + t_step);
+        for (; t0 < t_plain; t0 += t_step) step(std::false_type{});
+        for (; t0 < t_end; t0 += t_step) step(std::true_type{});
+      } else {
+        // Step x of this group of waves lies in slot x % n of its part of the ring.  The
+        // loads of a step past the group's last one go to the last one again, so that
+        // every wave issues the same number and a wait means the same for all.
+        const int all_steps = (t_end_tile - t0_tile + t_step - 1) / t_step;
+        const int t_last = t0 + max((t_end_tile - t0 + t_step - 1) / t_step - 1, 0) * t_step;
+        int t_in = min(t0, t_last);
+        int in = 0, out = 0;                 // slots that are loaded and used next
+        const uint8_t* ring = sh_mem;
+        auto fill = [&](auto wr_) __attribute__((always_inline)) {
+          constexpr int kWr = decltype(wr_)::value;
+          constexpr int kN = ring_steps(kSlots, kWr);
+          const Pages e = ahead;
+          const int tt = t_in;
+          t_in = min(t_in + t_step, t_last);
+          ahead = entries(t_in);
+          const uint32_t to = lds_address(ring) + in * (kBlocks * 1024);
+#pragma unroll
+          for (int i = 0; i < (kKB + kWr - 1) / kWr; ++i) {
+            const int blk = min(my_r + i * kWr, kKB - 1);
+            const int kt = blk / kJ;
+            copy_to_lds(k_block(e, tt, kt, blk - kt * kJ), to + blk * 1024);
+          }
+          const uint8_t* vp = v_base(e, tt);
+#pragma unroll
+          for (int i = 0; i < (kDT + kWr - 1) / kWr; ++i) {
+            const int dt = min(my_r + i * kWr, kDT - 1);
+            copy_to_lds(vp + (int64_t)dt * 16 * P * kEl, to + (kKB + dt) * 1024);
+          }
+          in = in + 1 == kN ? 0 : in + 1;
+        };
+        auto begin = [&](auto wr_) __attribute__((always_inline)) {
+          constexpr int kN = ring_steps(kSlots, decltype(wr_)::value);
+          ring = sh_mem + my_t * (kN * kBlocks * 1024);
+#pragma unroll
+          for (int i = 0; i < kN - 1; ++i) fill(wr_);
+        };
+        auto advance = [&](auto wr_) __attribute__((always_inline)) {
+          constexpr int kWr = decltype(wr_)::value;
+          constexpr int kN = ring_steps(kSlots, kWr);
+          constexpr int kLoads = (kKB + kWr - 1) / kWr + (kDT + kWr - 1) / kWr;
+          static_assert(kN >= 2 && (kN - 1) * kLoads <= 63, "ring depth");
+          wait_loads<(kN - 2) * kLoads>();
+          // every wave's part of the step has landed, and the slot that is filled next
+          // has been used up by all
+          bare_barrier();
+          fill(wr_);
+          slot = ring + out * (kBlocks * 1024);
+          out = out + 1 == kN ? 0 : out + 1;
+        };
+        typedef std::integral_constant<int, 4> Four;
+        typedef std::integral_constant<int, 2> Two;
+        if (wr == 4) begin(Four{});
+        else begin(Two{});
+        int x = 0;
+        auto next_step = [&](auto is_edge) __attribute__((always_inline)) {
+          if (wr == 4) advance(Four{});
+          else advance(Two{});
+          if (t0 < t_end) step(is_edge);
+          t0 += t_step;
+          ++x;
+        };
+        while (x < all_steps && t0 < t_plain) next_step(std::false_type{});
+        while (x < all_steps) next_step(std::true_type{});
+        wait_loads<0>();
+      }
       // Rows that see values that are not finite get them by products of indicators:
       // 1 where the value is +inf, -inf or NaN, with 1 where it is seen.
       if (__any(specials != 0u)) {
 #pragma unroll 1
         for (t0 = t_edge; t0 < t_end; t0 += t_step) {
-          load_v(check(entry(t0, vb)), t0);
+          load_v(entries(t0), t0);
           if (!__any(trim_values(false) != 0u)) continue;
-          uint32_t vis[NT];
+          Bits vis[NT];
           visible(vis);
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
@@ -578,9 +759,11 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sees[nt][i] = (spread(vis[nt], 8 * u + 2 * i) & E::kOne) |
-                              (spread(vis[nt], 8 * u + 2 * i + 1) & (E::kOne << 16));
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t v = (uint32_t)(vis[nt] >> vb);   // this lane's values
+                sees[nt][i] = (spread(v, 8 * u + 2 * i) & E::kOne) |
+                              (spread(v, 8 * u + 2 * i + 1) & (E::kOne << 16));
+              }
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) {
               const u32x4 x = F8 ? widen8<DT>(vf[dt], u) : vf[dt];
@@ -704,7 +887,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D)) void tree_attention_ke
 
 // Joins the parts of cut tiles.  Grid: (workgroups of the first launch, 16-row
 // blocks of a tile); the four waves take the parts in turn.
-template <int DT, int D, int NT, int TOK>
+template <int DT, int D, int NT, int TOK, bool RING>
 __global__ __launch_bounds__(kThreads) void tree_attention_join_kernel(
     const TreeAttnArgs a, const AttnCut* __restrict__ cuts, const float* __restrict__ part_ml,
     const float* __restrict__ part_o) {
@@ -717,7 +900,7 @@ __global__ __launch_bounds__(kThreads) void tree_attention_join_kernel(
   const AttnCut cut = cuts[b];
   if (cut.parts == 0) return;
   const int group = a.Hq / a.Hk;
-  const Req rq = request<NT, TOK>(a, cut.r, group);
+  const Req rq = request<NT, TOK, RING>(a, cut.r, group);
   const int row0 = cut.row_tile * (16 * NT * kWaves) + blk * 16;
   if (row0 >= rq.rows) return;
   const int lane = threadIdx.x & 63;
@@ -779,41 +962,40 @@ __global__ __launch_bounds__(kThreads) void tree_attention_join_kernel(
     a.lse[(int64_t)(rq.start + el) * a.Hq + y] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
-template <int DT, bool F8, int D, int NT>
+template <int DT, bool F8, int D, int NT, bool RING>
 dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   AttnCut* cuts = static_cast<AttnCut*>(a.ws);
   float* ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + p.cut_bytes);
   float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + p.cut_bytes + p.ml_bytes);
   // a step has 32 positions, 64 with an 8-bit cache
-  auto kernel = a.shift == 4        ? &tree_attention_kernel<DT, F8, D, NT, 4>
-                : F8 && a.shift == 5 ? &tree_attention_kernel<DT, F8, D, NT, F8 ? 5 : 0>
-                                     : &tree_attention_kernel<DT, F8, D, NT, 0>;
+  auto kernel = a.shift == 4         ? &tree_attention_kernel<DT, F8, D, NT, 4, RING>
+                : F8 && a.shift == 5 ? &tree_attention_kernel<DT, F8, D, NT, F8 ? 5 : 0, RING>
+                                     : &tree_attention_kernel<DT, F8, D, NT, 0, RING>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)p.groups), dim3(kThreads), 0, stream, a, cuts, ml, po);
   const dspark_status st = check_launch("tree_attention_kernel");
   if (st != DSPARK_OK) return st;
-  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, NT, F8 ? 64 : 32>),
+  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, NT, F8 ? 64 : 32, RING>),
                      dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kThreads), 0, stream, a,
                      cuts, ml, po);
   return check_launch("tree_attention_join_kernel");
+}
+template <int DT, bool F8, int D>
+dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  return p.ring      ? go<DT, F8, D, 2, true>(a, p, stream)
+         : p.nt == 1 ? go<DT, F8, D, 1, false>(a, p, stream)
+                     : go<DT, F8, D, 2, false>(a, p, stream);
 }
 
 }  // namespace
 
 template <int DT, bool F8>
 dspark_status run_tree_attention(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  const bool one = p.nt == 1;
   switch (a.D) {
-    case 64:
-      return one ? go<DT, F8, 64, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 64, 2>(a, p, stream)
-                                                               : go<DT, F8, 64, 4>(a, p, stream);
-    case 96:
-      return one ? go<DT, F8, 96, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 96, 2>(a, p, stream)
-                                                               : go<DT, F8, 96, 4>(a, p, stream);
-    case 128:
-      return one ? go<DT, F8, 128, 1>(a, p, stream) : p.nt == 2 ? go<DT, F8, 128, 2>(a, p, stream)
-                                                                : go<DT, F8, 128, 4>(a, p, stream);
-    case 192: return one ? go<DT, F8, 192, 1>(a, p, stream) : go<DT, F8, 192, 2>(a, p, stream);
-    default: return one ? go<DT, F8, 256, 1>(a, p, stream) : go<DT, F8, 256, 2>(a, p, stream);
+    case 64: return go<DT, F8, 64>(a, p, stream);
+    case 96: return go<DT, F8, 96>(a, p, stream);
+    case 128: return go<DT, F8, 128>(a, p, stream);
+    case 192: return go<DT, F8, 192>(a, p, stream);
+    default: return go<DT, F8, 256>(a, p, stream);
   }
 }
 
