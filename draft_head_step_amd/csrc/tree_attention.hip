@@ -33,8 +33,9 @@ AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64
   // variant runs any number of rows.
   const int64_t rows = (int64_t)((max_tokens + (int64_t)R - 1) / R) * group;
   p.nt = rows <= 8 ? 1 : 2;
-  p.ring = rows > 32;
-  const int per_cu = attn_waves(p.nt, D, p.ring);
+  p.ring = rows > (D <= 128 ? 32 : 8);
+  const int waves = attn_group(D, p.ring);
+  const int per_cu = attn_waves(p.nt, D, p.ring) * 4 / waves;   // four SIMDs
   int64_t groups = (int64_t)compute_units() * per_cu;
   if (capacity > 0) {
     // no more workgroups than units of work there can be
@@ -44,8 +45,8 @@ AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64
   }
   p.groups = (int)(groups < 1 ? 1 : groups);
   const int64_t blocks = ((int64_t)max_tokens * group + 15) / 16;
-  p.row_blocks = (int)(blocks < 4 * p.nt ? blocks : 4 * p.nt);
-  const size_t parts = (size_t)groups * 2 * 4 * p.nt;
+  p.row_blocks = (int)(blocks < waves * p.nt ? blocks : waves * p.nt);
+  const size_t parts = (size_t)groups * 2 * waves * p.nt;
   p.cut_bytes = ((size_t)groups * sizeof(AttnCut) + 255) / 256 * 256;
   p.ml_bytes = parts * 2 * 64 * sizeof(float);
   p.o_bytes = parts * 16 * (size_t)D * sizeof(float);

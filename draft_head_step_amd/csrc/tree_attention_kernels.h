@@ -31,10 +31,11 @@
 // reading those (without it the run with the most short requests ended last:
 // 64 chains over 37 to 8100 positions took 222 us, now 190).
 //
-// A workgroup's four waves share a tile of 16 NT WR rows: WR waves over rows,
-// 4 / WR over positions (interleaved steps).  A request's rows are cut into tiles
-// with WR = 4 and a last one whose WR goes by what is left, so that a chain of a
-// few drafts spreads over positions and a wide tree reads its cache once.
+// A workgroup's waves (four or eight) share a tile of 16 NT WR rows: WR waves over
+// rows, the others over positions (interleaved steps).  A request's rows are cut
+// into tiles with all waves over rows and a last one whose WR goes by what is left,
+// so that a chain of a few drafts spreads over positions and a wide tree reads its
+// cache once.
 //
 // Pages of at least a step's positions are the same for a whole wave: their
 // addresses are scalars (kPage = 0).  Smaller ones differ between lane groups:
@@ -54,7 +55,9 @@ namespace dspark {
 // A tile that a workgroup's run ends in: its parts are slot 2 * b + 1 of this
 // workgroup b and slots 2 * (b + 1), 2 * (b + 2), ... of the next ones.
 struct AttnCut {
-  int32_t r, h, row_tile, parts;   // parts = 0: none
+  int32_t parts;                   // 0: none
+  int32_t start, rows, row0, h;    // the request's first element and rows, the tile's first row
+  int32_t pad;
 };
 
 struct AttnPlan {
@@ -78,8 +81,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+// Waves of a workgroup: eight where they share a ring (a tile of 256 rows reads the
+// cache half as often as one of 128), four otherwise and for wide heads.
+constexpr int attn_group(int d, bool ring) { return ring && d <= 128 ? 8 : 4; }
+constexpr int kJoinWaves = 4;              // of the second launch
+constexpr int kJoinThreads = 64 * kJoinWaves;
 constexpr float kSlack = 8.0f;
 constexpr int kTileCost = 256;
 
@@ -193,12 +199,25 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The hardware's maximum as it is (the compiler's would make signalling NaN quiet
+// first); a NaN operand loses against a number.
+__device__ __forceinline__ float max2(float x, float y) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+
 // Over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false);
-  x = fmaxf(as_float(a[0]), as_float(a[1]));
+  x = max2(as_float(a[0]), as_float(a[1]));
   const auto b = __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false);
-  return fmaxf(as_float(b[0]), as_float(b[1]));
+  return max2(as_float(b[0]), as_float(b[1]));
 }
 __device__ __forceinline__ float groups_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -225,7 +244,7 @@ struct Req {
 __device__ __forceinline__ int tile_cost(int unit) {
   return unit < kTileCost ? kTileCost / unit : 1;
 }
-template <int NT, int TOK, bool RING>
+template <int NT, int TOK, int WAVES, bool RING>
 __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) {
   Req q;
   const int64_t s = a.cu[r], e = a.cu[r + 1];
@@ -239,22 +258,24 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) 
   q.bad = ctx < 0 || total > 0x7fff0000LL || pages_of(total < 0 ? 0 : total, a.shift) > a.max_pages;
   q.ctx = q.bad ? 0 : (int)ctx;
   q.total = q.bad ? 0 : (int)total;
-  constexpr int kTile = 16 * NT * kWaves;
+  constexpr int kTile = 16 * NT * WAVES;
   q.full = q.rows / kTile;
   const int rest = q.rows - q.full * kTile;
-  q.wr_last = rest == 0 ? 0 : !RING && rest <= 16 * NT ? 1 : rest <= 32 * NT ? 2 : 4;
+  // (a ring needs at least two waves for each copy)
+  q.wr_last = rest == 0 ? 0 : !RING && rest <= 16 * NT ? 1 : rest <= 32 * NT ? 2
+              : rest <= 64 * NT ? 4 : WAVES;
   // Units of a tile: its cost, then its steps.
   const int steps = q.bad ? 1 : (q.total + TOK - 1) / TOK;
   q.units_full = tile_cost(TOK) + steps;
-  const int wt = q.wr_last ? kWaves / q.wr_last : 1;
+  const int wt = q.wr_last ? WAVES / q.wr_last : 1;
   q.units_last = q.wr_last ? tile_cost(TOK * wt) + (steps + wt - 1) / wt : 0;
   return q;
 }
 
-// Steps of a ring of `slots` for each of 4 / wr groups of waves: at most four, so that
-// the loads in flight stay countable.
-constexpr int ring_steps(int slots, int wr) {
-  return slots * wr / kWaves < 4 ? slots * wr / kWaves : 4;
+// Steps of a ring of `slots` for each of `groups` of waves: at most four, so that the
+// loads in flight stay countable.
+constexpr int ring_steps(int slots, int groups) {
+  return slots / groups < 4 ? slots / groups : 4;
 }
 // Waves of a SIMD that the registers of a tile allow.
 constexpr int attn_waves(int nt, int d, bool ring) {
@@ -263,9 +284,11 @@ constexpr int attn_waves(int nt, int d, bool ring) {
 
 // Launch with kThreads threads; a run of units per workgroup.
 template <int DT, bool F8, int D, int NT, int kPage, bool kRing>
-__global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_attention_kernel(
+__global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)) void tree_attention_kernel(
     const TreeAttnArgs a, AttnCut* __restrict__ cuts, float* __restrict__ part_ml,
     float* __restrict__ part_o) {
+  constexpr int kWaves = attn_group(D, kRing);
+  constexpr int kThreads = 64 * kWaves;
   constexpr int kC = F8 ? 16 : 8;        // positions of a lane's 16 bytes of values
   constexpr int kTok = 4 * kC;           // positions of a step
   constexpr int kKT = kC / 4;            // key tiles of a step
@@ -279,16 +302,17 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
   // Where requests bring many rows the waves share positions (two or four of them)
   // and one copy of keys and values, in a ring of steps in LDS that is loaded up to
   // three steps ahead.  With few rows each wave loads its own positions into
-  // registers.  Two workgroups of a CU cover each other's waits either way.
-  constexpr int kRingBytes = D <= 128 ? 64 * 1024 : 128 * 1024;
+  // registers, and the workgroups of a CU cover each other's waits.
+  constexpr int kRingBytes = 128 * 1024;
   constexpr int kKB = kKT * kJ;          // 1 KB blocks of keys and of a step
   constexpr int kBlocks = kKB + kDT;
   constexpr int kSlots = kRingBytes / 1024 / kBlocks;
 
-  constexpr int kJoinBytes = 2 * NT * kDT * 64 * 16;
+  constexpr int kBufs = kWaves / 2;      // tiles that wait for their join at once
+  constexpr int kJoinBytes = kBufs * NT * kDT * 64 * 16;
   __shared__ __align__(16) uint8_t sh_mem[kRing && kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes];
-  f32x4(&sh_o)[2][NT * kDT][64] = *reinterpret_cast<f32x4(*)[2][NT * kDT][64]>(sh_mem);
-  __shared__ float sh_ml[2][NT][2][64];
+  f32x4(&sh_o)[kBufs][NT * kDT][64] = *reinterpret_cast<f32x4(*)[kBufs][NT * kDT][64]>(sh_mem);
+  __shared__ float sh_ml[kBufs][NT][2][64];
   __shared__ int64_t sh_scan[kWaves];
   __shared__ int64_t sh_pos[2];          // request and unit within it of this run's first unit
 
@@ -311,7 +335,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
     const int per = (a.R + kThreads - 1) / kThreads;
     const int r0 = min(t * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok, kRing>(a, r, group).head_units();
+    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group).head_units();
     int64_t inc = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -333,7 +357,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
     int64_t first = pre + inc - mine;
     if (w < w_end && w >= first && w < first + mine) {
       for (int r = r0; r < r1; ++r) {
-        const int64_t u = a.Hk * request<NT, kTok, kRing>(a, r, group).head_units();
+        const int64_t u = a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group).head_units();
         if (w < first + u) {
           sh_pos[0] = r;
           sh_pos[1] = w - first;
@@ -345,30 +369,28 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
     __syncthreads();
   }
   if (w >= w_end) {
-    if (t == 0) cuts[b] = AttnCut{0, 0, 0, 0};
+    if (t == 0) cuts[b] = AttnCut{0, 0, 0, 0, 0, 0};
     return;
   }
   int r = uni((int)sh_pos[0]);
-  int64_t at = sh_pos[1];
-  AttnCut cut = {0, 0, 0, 0};
+  AttnCut cut = {0, 0, 0, 0, 0, 0};
+  Req rq = request<NT, kTok, kWaves, kRing>(a, r, group);
+  // the first tile by division, the others by counting
+  int h, row_tile, s0;
+  {
+    const int64_t at = sh_pos[1], per_head = rq.head_units();
+    h = uni((int)(at / per_head));
+    const int64_t in_head = at - h * per_head;
+    row_tile = uni(in_head < (int64_t)rq.full * rq.units_full ? (int)(in_head / rq.units_full) : rq.full);
+    s0 = uni((int)(in_head - (int64_t)row_tile * rq.units_full));
+  }
 
   while (w < w_end) {
-    const Req rq = request<NT, kTok, kRing>(a, r, group);
-    const int64_t per_head = rq.head_units();
-    if (at >= a.Hk * per_head) {   // also requests without work
-      at -= a.Hk * per_head;
-      ++r;
-      continue;
-    }
     // ---- this segment: units s0 .. s1 of row tile `row_tile` of head h ----
     if (kRing) __syncthreads();            // the ring is free
-    const int h = uni((int)(at / per_head));
-    const int64_t in_head = at - h * per_head;
-    const bool full = in_head < (int64_t)rq.full * rq.units_full;
-    const int row_tile = uni(full ? (int)(in_head / rq.units_full) : rq.full);
+    const bool full = row_tile < rq.full;
     const int units = uni(full ? rq.units_full : rq.units_last);
     const int wr = uni(full ? kWaves : rq.wr_last);
-    const int s0 = uni((int)(in_head - (int64_t)row_tile * rq.units_full));
     const int64_t left = w_end - w;
     const int s1 = uni((int)(left < units - s0 ? s0 + left : units));
     const int wt = kWaves / wr;
@@ -400,6 +422,19 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
           if (in && d < D) x = *reinterpret_cast<const u32x4*>(qp + d);
           qf[nt][j * kMj + i] = x ^ flip;
         }
+    }
+    // Mask rows of up to 64 nodes are read here: a load among the steps would wait for
+    // every copy to LDS before it.
+    const bool short_mask = a.mask && a.mask_words <= 2;
+    uint64_t mask64[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mask64[nt] = 0;
+      if (short_mask) {
+        const uint32_t* mw = a.mask + (int64_t)(rq.start + el[nt]) * a.mask_words;
+        mask64[nt] = mw[0];
+        if (a.mask_words == 2) mask64[nt] |= (uint64_t)mw[1] << 32;
+      }
     }
     f32x4 o[NT][kDT];
     float m[NT], l[NT];
@@ -451,17 +486,25 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
         typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
         const scalar_ptr row = (scalar_ptr)(uintptr_t)pages;
         const int i = tt >> shift;
-        // A page outside the pool is not touched: page 0 stands in, and the rows are NaN.
         auto one = [&](int k) __attribute__((always_inline)) {
-          const int32_t p = row[min(i + k, last_page)];
-          const bool ok = page_ok(p, a.num_pages);
-          bad |= !ok;
-          return (uint64_t)(uint32_t)(ok ? p : 0);
+          return (uint64_t)(uint32_t)row[min(i + k, last_page)];
         };
         Pages e = {one(0), 0};
         if constexpr (kPk >= 2) e.lo |= one(1) << 32;
         if constexpr (kPk == 4) e.hi = one(2) | one(3) << 32;
         return e;
+      };
+      // A page outside the pool is not touched: page 0 stands in, and the rows are NaN.
+      auto check = [&](Pages e) __attribute__((always_inline)) {
+        auto one = [&](int k) __attribute__((always_inline)) {
+          const bool ok = page_ok((int32_t)e.at(k), a.num_pages);
+          bad |= !ok;
+          return ok ? (uint64_t)(uint32_t)e.at(k) : (uint64_t)0;
+        };
+        Pages c = {one(0), 0};
+        if constexpr (kPk >= 2) c.lo |= one(1) << 32;
+        if constexpr (kPk == 4) c.hi = one(2) | one(3) << 32;
+        return c;
       };
       // Addresses of this lane's 16 bytes of key block (kt, j) and of value block dt of
       // the step at tt.
@@ -520,9 +563,14 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
             const uint32_t* mw = a.mask + (int64_t)(rq.start + el[nt]) * a.mask_words;
             const int jj = j0 < 0 ? 0 : j0;
             const int w0 = jj >> 5, sh = jj & 31;
+            uint64_t two;
             auto word = [&](int w) { return w < a.mask_words ? (uint64_t)mw[w] : (uint64_t)0; };
-            uint64_t two = (word(w0) | word(w0 + 1) << 32) >> sh;
-            if (F8) two |= sh ? word(w0 + 2) << (64 - sh) : (uint64_t)0;
+            if (short_mask) {
+              two = jj < 64 ? mask64[nt] >> jj : 0;
+            } else {
+              two = (word(w0) | word(w0 + 1) << 32) >> sh;
+              if (F8) two |= sh ? word(w0 + 2) << (64 - sh) : (uint64_t)0;
+            }
             bits = (Bits)two;
             if (j0 < 0) bits = -j0 < kTok ? bits << -j0 : (Bits)0;
           } else {
@@ -564,7 +612,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
         const int next = t0 + t_step;
         Pages now;
         if constexpr (!kRing) {
-          now = ahead;
+          now = check(ahead);
           ahead = entries(next + t_step);
         } else {
 #pragma unroll
@@ -606,24 +654,40 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
                 s[nt][kt][i] = as_float((as_bits(s[nt][kt][i]) & on) | (0xff800000u & ~on));
               }
         }
+        if constexpr (kRing) {
+          // read before the exponentials, so that they cover the latency
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt)
+            vf[dt] = *reinterpret_cast<const u32x4*>(slot + (kKB + dt) * 1024 + lane * 16);
+          asm volatile("" ::: "memory");
+        }
         // ---- probabilities ----
-        u32x4 pf[NT][kU];
+        float top[NT];
+        bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float top = s[nt][0][0];
+          float x = max2(s[nt][0][0], s[nt][0][1]);
+          x = max3(x, s[nt][0][2], s[nt][0][3]);
 #pragma unroll
-          for (int kt = 0; kt < kKT; ++kt)
+          for (int kt = 1; kt < kKT; ++kt)
+            x = max3(max3(x, s[nt][kt][0], s[nt][kt][1]), s[nt][kt][2], s[nt][kt][3]);
+          top[nt] = groups_max(x) * sc;
+          rise |= top[nt] > m[nt] + kSlack;
+        }
+        if (__any(rise)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[nt][kt][i]);
-          top = groups_max(top) * sc;
-          if (__any(top > m[nt] + kSlack)) {
-            const float nm = fmaxf(m[nt], top);
+          for (int nt = 0; nt < NT; ++nt) {
+            const float nm = top[nt] > m[nt] + kSlack ? top[nt] : m[nt];
             const float f = m[nt] == nm ? 1.0f : pow2(m[nt] - nm);
             l[nt] *= f;
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) o[nt][dt] *= f;
             m[nt] = nm;
           }
+        }
+        u32x4 pf[NT][kU];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           const float base = m[nt] == -INFINITY ? 0.0f : m[nt];
           uint32_t lo[kKT], hi[kKT];   // a tile's four probabilities, packed
           float sum = 0.0f;
@@ -635,8 +699,8 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
               p[i] = pow2(fmaf(s[nt][kt][i], sc, -base));
               // unseen: 0 whatever the line above made of -inf
               if (kEdge) p[i] = as_float(as_bits(p[i]) & spread(mine(vis[nt], kt), i));
-              sum += p[i];
             }
+            sum += (p[0] + p[1]) + (p[2] + p[3]);
             lo[kt] = E::pack(p[0], p[1]);
             hi[kt] = E::pack(p[2], p[3]);
           }
@@ -648,11 +712,6 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
             pf[nt][u] = u32x4{lo[2 * u], hi[2 * u], lo[2 * u + 1], hi[2 * u + 1]};
         }
         // ---- values ----
-        if constexpr (kRing) {
-#pragma unroll
-          for (int dt = 0; dt < kDT; ++dt)
-            vf[dt] = *reinterpret_cast<const u32x4*>(slot + (kKB + dt) * 1024 + lane * 16);
-        }
         if constexpr (kEdge) {
           // A value that is not finite must not meet the zero probability of a row that
           // does not see it: it leaves the product here and comes back below.
@@ -672,7 +731,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
       int t_edge = max(t_plain, 0);
       t_edge = t0 >= t_edge ? t0 : t0 + (t_edge - t0 + t_step - 1) / t_step * t_step;
       if constexpr (!kRing) {
-        const Pages first = ahead;
+        const Pages first = check(ahead);
         load_k(first, t0);
         load_v(first, t0);
         ahead = entries(t0 + t_step);
@@ -689,8 +748,8 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
         const uint8_t* ring = sh_mem;
         auto fill = [&](auto wr_) __attribute__((always_inline)) {
           constexpr int kWr = decltype(wr_)::value;
-          constexpr int kN = ring_steps(kSlots, kWr);
-          const Pages e = ahead;
+          constexpr int kN = ring_steps(kSlots, kWaves / kWr);
+          const Pages e = check(ahead);
           const int tt = t_in;
           t_in = min(t_in + t_step, t_last);
           ahead = entries(t_in);
@@ -710,14 +769,14 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
           in = in + 1 == kN ? 0 : in + 1;
         };
         auto begin = [&](auto wr_) __attribute__((always_inline)) {
-          constexpr int kN = ring_steps(kSlots, decltype(wr_)::value);
+          constexpr int kN = ring_steps(kSlots, kWaves / decltype(wr_)::value);
           ring = sh_mem + my_t * (kN * kBlocks * 1024);
 #pragma unroll
           for (int i = 0; i < kN - 1; ++i) fill(wr_);
         };
         auto advance = [&](auto wr_) __attribute__((always_inline)) {
           constexpr int kWr = decltype(wr_)::value;
-          constexpr int kN = ring_steps(kSlots, kWr);
+          constexpr int kN = ring_steps(kSlots, kWaves / kWr);
           constexpr int kLoads = (kKB + kWr - 1) / kWr + (kDT + kWr - 1) / kWr;
           static_assert(kN >= 2 && (kN - 1) * kLoads <= 63, "ring depth");
           wait_loads<(kN - 2) * kLoads>();
@@ -728,13 +787,16 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
           slot = ring + out * (kBlocks * 1024);
           out = out + 1 == kN ? 0 : out + 1;
         };
+        typedef std::integral_constant<int, kWaves> Eight;   // or four, not used
         typedef std::integral_constant<int, 4> Four;
         typedef std::integral_constant<int, 2> Two;
-        if (wr == 4) begin(Four{});
+        if (kWaves == 8 && wr == 8) begin(Eight{});
+        else if (wr == 4) begin(Four{});
         else begin(Two{});
         int x = 0;
         auto next_step = [&](auto is_edge) __attribute__((always_inline)) {
-          if (wr == 4) advance(Four{});
+          if (kWaves == 8 && wr == 8) advance(Eight{});
+          else if (wr == 4) advance(Four{});
           else advance(Two{});
           if (t0 < t_end) step(is_edge);
           t0 += t_step;
@@ -749,7 +811,7 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
       if (__any(specials != 0u)) {
 #pragma unroll 1
         for (t0 = t_edge; t0 < t_end; t0 += t_step) {
-          load_v(entries(t0), t0);
+          load_v(check(entries(t0)), t0);
           if (!__any(trim_values(false) != 0u)) continue;
           Bits vis[NT];
           visible(vis);
@@ -802,9 +864,9 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
       for (int nt = 0; nt < NT; ++nt) l[nt] = NAN;
     }
 
-    // ---- join the waves over positions: wt = 4, 2, 1 ----
+    // ---- join the waves over positions ----
     for (int half = wt >> 1; half >= 1; half >>= 1) {
-      // buffers: wr * half <= 2
+      // buffers: wr * half <= kWaves / 2
       const int buf = (my_t & (half - 1)) * wr + my_r;
       __syncthreads();
       if (my_t >= half && my_t < 2 * half) {
@@ -874,92 +936,98 @@ __global__ __launch_bounds__(kThreads, attn_waves(NT, D, kRing)) void tree_atten
       const int64_t last = w + (units - 1);
       int64_t owner = last * runs / all;
       while (all * (owner + 1) / runs <= last) ++owner;
-      cut.r = r;
-      cut.h = h;
-      cut.row_tile = row_tile;
       cut.parts = (int)(owner - b) + 1;
+      cut.start = rq.start;
+      cut.rows = rq.rows;
+      cut.row0 = row_tile * (16 * NT * kWaves);
+      cut.h = h;
     }
     w += s1 - s0;
-    at += s1 - s0;
+    if (w >= w_end) break;
+    // the next tile: of this head, of the next one, of the next request with rows
+    s0 = 0;
+    ++row_tile;
+    if (row_tile >= rq.full + (rq.wr_last > 0 ? 1 : 0)) {
+      row_tile = 0;
+      ++h;
+    }
+    if (h >= a.Hk) {
+      h = 0;
+      do rq = request<NT, kTok, kWaves, kRing>(a, ++r, group);
+      while (rq.rows == 0);                // there is one: units are left
+    }
   }
   if (t == 0) cuts[b] = cut;
 }
 
 // Joins the parts of cut tiles.  Grid: (workgroups of the first launch, 16-row
-// blocks of a tile); the four waves take the parts in turn.
-template <int DT, int D, int NT, int TOK, bool RING>
-__global__ __launch_bounds__(kThreads) void tree_attention_join_kernel(
+// blocks of a tile).  Each of the four waves joins its share of the channels over
+// all parts, four parts' loads at a time; no wave waits for another.
+template <int DT, int D, int BLOCKS>
+__global__ __launch_bounds__(kJoinThreads) void tree_attention_join_kernel(
     const TreeAttnArgs a, const AttnCut* __restrict__ cuts, const float* __restrict__ part_ml,
     const float* __restrict__ part_o) {
   constexpr int kDT = D / 16;
+  constexpr int kMine = (kDT + kJoinWaves - 1) / kJoinWaves;
+  constexpr int kAhead = 4;
   using E = El<DT>;
-  __shared__ f32x4 sh_o[kWaves - 1][kDT][64];
-  __shared__ float sh_ml[kWaves - 1][2][64];
   const int b = blockIdx.x;
   const int blk = blockIdx.y;
   const AttnCut cut = cuts[b];
-  if (cut.parts == 0) return;
-  const int group = a.Hq / a.Hk;
-  const Req rq = request<NT, TOK, RING>(a, cut.r, group);
-  const int row0 = cut.row_tile * (16 * NT * kWaves) + blk * 16;
-  if (row0 >= rq.rows) return;
+  const int row0 = cut.row0 + blk * 16;
+  if (cut.parts == 0 || row0 >= cut.rows) return;
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int dt0 = uni(threadIdx.x >> 6) * kMine;
+  if (dt0 >= kDT) return;
   float m = -INFINITY, l = 0.0f;
-  f32x4 o[kDT];
+  f32x4 o[kMine];
 #pragma unroll
-  for (int dt = 0; dt < kDT; ++dt) o[dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p = wave; p < cut.parts; p += kWaves) {
-    const int64_t slot = p == 0 ? 2 * (int64_t)b + 1 : 2 * (int64_t)(b + p);
-    const int64_t at = slot * kWaves * NT + blk;
-    const float m2 = part_ml[(at * 2) * 64 + lane], l2 = part_ml[(at * 2 + 1) * 64 + lane];
-    const f32x4* po = reinterpret_cast<const f32x4*>(part_o) + at * kDT * 64;
-    f32x4 x[kDT];
+  for (int d = 0; d < kMine; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p0 = 0; p0 < cut.parts; p0 += kAhead) {
+    float m2[kAhead], l2[kAhead];
+    f32x4 x[kAhead][kMine];
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt) x[dt] = po[dt * 64 + lane];
-    const float nm = fmaxf(m, m2);
-    const float base = nm == -INFINITY ? 0.0f : nm;
-    const float f1 = pow2(m - base), f2 = pow2(m2 - base);
-    m = nm;
-    l = l * f1 + l2 * f2;
+    for (int u = 0; u < kAhead; ++u) {
+      const int p = min(p0 + u, cut.parts - 1);
+      const int64_t slot = p == 0 ? 2 * (int64_t)b + 1 : 2 * (int64_t)(b + p);
+      const int64_t at = slot * BLOCKS + blk;
+      m2[u] = part_ml[(at * 2) * 64 + lane];
+      l2[u] = part_ml[(at * 2 + 1) * 64 + lane];
+      const f32x4* po = reinterpret_cast<const f32x4*>(part_o) + at * kDT * 64 + lane;
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt) o[dt] = o[dt] * f1 + x[dt] * f2;
-  }
-  if (wave > 0) {
-    sh_ml[wave - 1][0][lane] = m;
-    sh_ml[wave - 1][1][lane] = l;
+      for (int d = 0; d < kMine; ++d) x[u][d] = po[min(dt0 + d, kDT - 1) * 64];
+    }
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt) sh_o[wave - 1][dt][lane] = o[dt];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-  for (int v = 0; v < kWaves - 1; ++v) {
-    const float m2 = sh_ml[v][0][lane], l2 = sh_ml[v][1][lane];
-    const float nm = fmaxf(m, m2);
-    const float base = nm == -INFINITY ? 0.0f : nm;
-    const float f1 = pow2(m - base), f2 = pow2(m2 - base);
-    m = nm;
-    l = l * f1 + l2 * f2;
+    for (int u = 0; u < kAhead; ++u) {
+      if (p0 + u >= cut.parts) continue;
+      const float nm = fmaxf(m, m2[u]);
+      const float base = nm == -INFINITY ? 0.0f : nm;
+      const float f1 = pow2(m - base), f2 = pow2(m2[u] - base);
+      m = nm;
+      l = l * f1 + l2[u] * f2;
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt) o[dt] = o[dt] * f1 + sh_o[v][dt][lane] * f2;
+      for (int d = 0; d < kMine; ++d) o[d] = o[d] * f1 + x[u][d] * f2;
+    }
   }
   const int col = lane & 15, g = lane >> 4;
   const int row = row0 + col;
-  if (row >= rq.rows) return;
+  if (row >= cut.rows) return;
+  const int group = a.Hq / a.Hk;
   const int el = row / group;
   const int y = cut.h * group + row - el * group;
   const float vs = a.v_scale ? a.v_scale[cut.h] : 1.0f;
   const float f = l == 0.0f ? 0.0f : vs / l;
-  uint16_t* op = static_cast<uint16_t*>(a.out) + (int64_t)(rq.start + el) * a.out_stride + y * D + g * 4;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + (int64_t)(cut.start + el) * a.out_stride + y * D + g * 4;
 #pragma unroll
-  for (int dt = 0; dt < kDT; ++dt) {
+  for (int d = 0; d < kMine; ++d) {
+    if (dt0 + d >= kDT) break;
     uint2 x;
-    x.x = E::pack(o[dt][0] * f, o[dt][1] * f);
-    x.y = E::pack(o[dt][2] * f, o[dt][3] * f);
-    *reinterpret_cast<uint2*>(op + dt * 16) = x;
+    x.x = E::pack(o[d][0] * f, o[d][1] * f);
+    x.y = E::pack(o[d][2] * f, o[d][3] * f);
+    *reinterpret_cast<uint2*>(op + (dt0 + d) * 16) = x;
   }
-  if (a.lse && g == 0)
-    a.lse[(int64_t)(rq.start + el) * a.Hq + y] = (m + __log2f(l)) * 0.69314718055994531f;
+  if (a.lse && g == 0 && dt0 == 0)
+    a.lse[(int64_t)(cut.start + el) * a.Hq + y] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 template <int DT, bool F8, int D, int NT, bool RING>
@@ -971,11 +1039,12 @@ dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   auto kernel = a.shift == 4         ? &tree_attention_kernel<DT, F8, D, NT, 4, RING>
                 : F8 && a.shift == 5 ? &tree_attention_kernel<DT, F8, D, NT, F8 ? 5 : 0, RING>
                                      : &tree_attention_kernel<DT, F8, D, NT, 0, RING>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)p.groups), dim3(kThreads), 0, stream, a, cuts, ml, po);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.groups), dim3(64 * attn_group(D, RING)), 0, stream, a,
+                     cuts, ml, po);
   const dspark_status st = check_launch("tree_attention_kernel");
   if (st != DSPARK_OK) return st;
-  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, NT, F8 ? 64 : 32, RING>),
-                     dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kThreads), 0, stream, a,
+  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, attn_group(D, RING) * NT>),
+                     dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kJoinThreads), 0, stream, a,
                      cuts, ml, po);
   return check_launch("tree_attention_join_kernel");
 }
