@@ -2,14 +2,22 @@
 //
 //   kv_store:  K and V rows of new elements into their slots.  The keys keep 16
 //              bytes (c elements) of a row together, [D / c][P][c]; the values
-//              lie transposed, [D][P].  A workgroup takes 16 elements of one
-//              head: rows are read 16 bytes a lane, pass through LDS, and are
-//              written with neighbouring lanes on neighbouring elements, which
-//              in a run of slots are neighbouring addresses in both caches.
+//              lie transposed, [D][P].  A workgroup takes 16 or 64 elements of
+//              one head: rows are read 16 bytes a lane, pass through LDS, and
+//              are written with neighbouring lanes on neighbouring elements,
+//              which in a run of slots are neighbouring addresses in both
+//              caches.  Prompts take 64, so that a value channel's piece is
+//              whole lines written at once, steps 16, for more workgroups.
 //   kv_commit: the accepted path's keys and values to the front.  A thread
-//              owns one 16-byte piece of the keys or one value channel and moves
-//              it for i = 1, 2, ... in turn.  path[i] >= i and path increases,
-//              so position i, once written, is no later source.
+//              owns 16-byte pieces of the keys and value channels and moves each
+//              for i = 1, 2, ... in turn, four positions' loads at a time.
+//              path[i] >= i and path increases, so position i, once written, is
+//              no later source.  Places in the cache are worked out once per
+//              request, in LDS.  A value channel's positions are neighbours, so a
+//              moved byte touches a whole 64-byte piece of memory on both sides:
+//              that, not the bytes moved, is what the call costs.
+#include <type_traits>
+
 #include "dspark_internal.h"
 #include "paged.h"
 
@@ -19,7 +27,6 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kT = 256;
-constexpr int kTok = 16;   // elements per workgroup
 
 __device__ __forceinline__ float widen(uint16_t x, bool bf) {
   return bf ? __builtin_bit_cast(float, (uint32_t)x << 16)
@@ -34,7 +41,7 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
 }
 
 // Grid: (ceil(max_tokens / kTok), Hk).  F8: 8-bit cache of 16-bit inputs.
-template <int D, bool F8>
+template <int D, bool F8, int kTok>
 __global__ __launch_bounds__(kT) void kv_store_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride,
     int64_t v_stride, int bf, const int64_t* __restrict__ slots, const int32_t* __restrict__ count,
@@ -93,6 +100,9 @@ __global__ __launch_bounds__(kT) void kv_store_kernel(
   }
 }
 
+constexpr int kMoves = 64;   // positions whose places are in LDS at once
+constexpr int kAhead = 4;    // of them, loaded before the first is stored
+
 // Grid: (R, layers).  One workgroup moves all heads of one request and layer.
 template <int EL>
 __global__ __launch_bounds__(kT) void kv_commit_kernel(
@@ -101,7 +111,10 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
     const int32_t* __restrict__ path, const int32_t* __restrict__ accepted, int max_nodes, int Hk,
     int D, int shift, int max_pages, int num_pages, int32_t* __restrict__ new_len) {
   constexpr int kC = 16 / EL;
-  __shared__ int bad;
+  typedef std::conditional_t<EL == 1, uint8_t, uint16_t> V;
+  __shared__ int bad, moves;
+  // element offsets of head 0, channel 0 of both ends in the two caches
+  __shared__ int64_t k_from[kMoves], k_to[kMoves], v_from[kMoves], v_to[kMoves];
   const int t = threadIdx.x;
   const int r = blockIdx.x;
   const int32_t* row = path + (size_t)r * max_nodes;
@@ -109,7 +122,7 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
   const int64_t ctx = ctx_len[r];
   const int acc = accepted[r];
   const int64_t room = (int64_t)max_pages << shift;
-  if (t == 0) bad = 0;
+  if (t == 0) bad = moves = 0;
   __syncthreads();
   const bool range = ctx >= 0 && acc >= -1 && acc < max_nodes && ctx + 1 + acc <= room;
   if (!range) {
@@ -121,49 +134,94 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
         fine = page_ok(pages[(ctx + row[i]) >> shift], num_pages) &&
                page_ok(pages[(ctx + i) >> shift], num_pages);
       if (!fine) atomicOr(&bad, 1);
+      if (row[i] != i) atomicOr(&moves, 1);
     }
   }
   __syncthreads();
   const bool skip = bad != 0;
   if (blockIdx.y == 0 && t == 0) new_len[r] = skip ? -1 : (int32_t)(ctx + 1 + acc);
-  if (skip) return;
+  if (skip || !moves) return;   // a chain's path is where it belongs
   uint8_t* kc = k_cache + (int64_t)blockIdx.y * k_layer * EL;
-  uint8_t* vc = v_cache + (int64_t)blockIdx.y * v_layer * EL;
-  const int pieces = Hk * (D / kC);
+  V* vc = reinterpret_cast<V*>(v_cache + (int64_t)blockIdx.y * v_layer * EL);
   const int m = (1 << shift) - 1;
-  for (int w = t; w < pieces + Hk * D; w += kT) {
-    const bool key = w < pieces;
-    const int h = key ? w / (D / kC) : (w - pieces) / D;
-    const int d = key ? (w - h * (D / kC)) * kC : (w - pieces) - h * D;
-    for (int i = 1; i <= acc; ++i) {
-      const int64_t from = ctx + row[i], to = ctx + i;
-      if (from == to) continue;
+  const int k_pieces = Hk * (D / kC);
+  for (int i0 = 1; i0 <= acc; i0 += kMoves) {
+    const int n = min(kMoves, acc - i0 + 1);
+    __syncthreads();
+    if (t < n) {
+      const int64_t from = ctx + row[i0 + t], to = ctx + i0 + t;
       const int64_t fp = pages[from >> shift], tp = pages[to >> shift];
-      const int fo = (int)(from & m), to_ = (int)(to & m);
-      if (key) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(kc + k_offset(fp, h, d, fo, Hk, D, shift, kC) * EL);
-        *reinterpret_cast<u32x4*>(kc + k_offset(tp, h, d, to_, Hk, D, shift, kC) * EL) = x;
-      } else if (EL == 1) {
-        vc[v_offset(tp, h, d, to_, Hk, D, shift)] = vc[v_offset(fp, h, d, fo, Hk, D, shift)];
-      } else {
-        uint16_t* vw = reinterpret_cast<uint16_t*>(vc);
-        vw[v_offset(tp, h, d, to_, Hk, D, shift)] = vw[v_offset(fp, h, d, fo, Hk, D, shift)];
+      k_from[t] = k_offset(fp, 0, 0, (int)(from & m), Hk, D, shift, kC);
+      k_to[t] = k_offset(tp, 0, 0, (int)(to & m), Hk, D, shift, kC);
+      v_from[t] = v_offset(fp, 0, 0, (int)(from & m), Hk, D, shift);
+      v_to[t] = v_offset(tp, 0, 0, (int)(to & m), Hk, D, shift);
+    }
+    __syncthreads();
+    // pieces of one head follow each other at a page's distance, and so do the heads
+    for (int w = t; w < k_pieces; w += kT) {
+      const int64_t at = ((int64_t)w << shift) * kC;
+      for (int i = 0; i < n; i += kAhead) {
+        u32x4 x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          x[u] = *reinterpret_cast<const u32x4*>(kc + (k_from[min(i + u, n - 1)] + at) * EL);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (i + u < n) *reinterpret_cast<u32x4*>(kc + (k_to[i + u] + at) * EL) = x[u];
+      }
+    }
+    for (int w = t; w < Hk * D; w += 2 * kT) {
+      const int64_t a0 = (int64_t)w << shift;
+      const bool two = w + kT < Hk * D;
+      const int64_t a1 = two ? (int64_t)(w + kT) << shift : a0;
+      for (int i = 0; i < n; i += kAhead) {
+        V x[kAhead], y[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t f = v_from[min(i + u, n - 1)];
+          x[u] = vc[f + a0];
+          y[u] = vc[f + a1];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (i + u < n) {
+            vc[v_to[i + u] + a0] = x[u];
+            if (two) vc[v_to[i + u] + a1] = y[u];
+          }
+        }
       }
     }
   }
 }
 
+struct StoreArgs {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t k_stride, v_stride;
+  int bf;
+  const int64_t* slots;
+  const int32_t* count;
+  int n, Hk, shift, num_pages;
+  const float* k_scale;
+  const float* v_scale;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+};
+
+template <int D, bool F8, int kTok>
+void store(const StoreArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)a.n + kTok - 1) / kTok), (unsigned)a.Hk);
+  hipLaunchKernelGGL((kv_store_kernel<D, F8, kTok>), grid, dim3(kT), 0, stream, a.k, a.v,
+                     a.k_stride, a.v_stride, a.bf, a.slots, a.count, a.n, a.Hk, a.shift,
+                     a.num_pages, a.k_scale, a.v_scale, a.k_cache, a.v_cache);
+}
+
 template <int D>
-void store_d(bool f8, dim3 grid, hipStream_t stream, const uint16_t* k, const uint16_t* v,
-             int64_t ks, int64_t vs, int bf, const int64_t* slots, const int32_t* count, int n,
-             int Hk, int shift, int num_pages, const float* k_scale, const float* v_scale,
-             uint8_t* kc, uint8_t* vc) {
-  if (f8)
-    hipLaunchKernelGGL((kv_store_kernel<D, true>), grid, dim3(kT), 0, stream, k, v, ks, vs, bf,
-                       slots, count, n, Hk, shift, num_pages, k_scale, v_scale, kc, vc);
-  else
-    hipLaunchKernelGGL((kv_store_kernel<D, false>), grid, dim3(kT), 0, stream, k, v, ks, vs, bf,
-                       slots, count, n, Hk, shift, num_pages, k_scale, v_scale, kc, vc);
+void store_d(bool f8, const StoreArgs& a, hipStream_t stream) {
+  // 64 elements a workgroup where that leaves four of them for every CU
+  const bool many = (int64_t)a.n * a.Hk >= 64 * 1024;
+  if (f8) many ? store<D, true, 64>(a, stream) : store<D, true, 16>(a, stream);
+  else many ? store<D, false, 64>(a, stream) : store<D, false, 16>(a, stream);
 }
 
 }  // namespace
@@ -173,19 +231,17 @@ dspark_status launch_kv_store(const void* k, const void* v, int64_t k_stride, in
                               int max_tokens, int Hk, int D, int shift, int num_pages,
                               int cache_dtype, const float* k_scale, const float* v_scale,
                               void* k_cache, void* v_cache, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)max_tokens + kTok - 1) / kTok), (unsigned)Hk);
   const bool f8 = cache_dtype == DSPARK_E4M3;
-  auto go = [&](auto store) {
-    store(f8, grid, stream, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-          k_stride, v_stride, dtype == DSPARK_BF16, slots, count, max_tokens, Hk, shift, num_pages,
-          k_scale, v_scale, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache));
-  };
+  const StoreArgs a = {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride,
+                       v_stride, dtype == DSPARK_BF16, slots, count, max_tokens, Hk, shift,
+                       num_pages, k_scale, v_scale, static_cast<uint8_t*>(k_cache),
+                       static_cast<uint8_t*>(v_cache)};
   switch (D) {
-    case 64: go(&store_d<64>); break;
-    case 96: go(&store_d<96>); break;
-    case 128: go(&store_d<128>); break;
-    case 192: go(&store_d<192>); break;
-    default: go(&store_d<256>); break;
+    case 64: store_d<64>(f8, a, stream); break;
+    case 96: store_d<96>(f8, a, stream); break;
+    case 128: store_d<128>(f8, a, stream); break;
+    case 192: store_d<192>(f8, a, stream); break;
+    default: store_d<256>(f8, a, stream); break;
   }
   return check_launch("kv_store_kernel");
 }

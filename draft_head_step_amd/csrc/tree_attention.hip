@@ -37,10 +37,13 @@ AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64
   const int waves = attn_group(D, p.ring);
   const int per_cu = attn_waves(p.nt, D, p.ring) * 4 / waves;   // four SIMDs
   int64_t groups = (int64_t)compute_units() * per_cu;
+  // Up to 512 positions a tile is at most four steps of every wave: cutting it would
+  // cost more than it spreads.
+  p.whole = capacity > 0 && capacity <= 512;
   if (capacity > 0) {
     // no more workgroups than units of work there can be
     const int64_t tiles = ((int64_t)max_tokens * group + 16 * p.nt - 1) / (16 * p.nt) + R;
-    const int64_t units = tiles * Hk * ((capacity + 31) / 32);
+    const int64_t units = tiles * Hk * (p.whole ? 1 : (capacity + 31) / 32);
     if (units < groups) groups = units;
   }
   p.groups = (int)(groups < 1 ? 1 : groups);

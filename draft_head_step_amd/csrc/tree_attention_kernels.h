@@ -29,7 +29,9 @@
 // lengths itself.  A tile counts for kTileCost positions more than it has: the
 // queries, the first loads and the last sums of a tile take about as long as
 // reading those (without it the run with the most short requests ended last:
-// 64 chains over 37 to 8100 positions took 222 us, now 190).
+// 64 chains over 37 to 8100 positions took 222 us, then 201).  Where the table has
+// room for few positions a tile is one unit, nothing is cut, and the second launch
+// is left out.
 //
 // A workgroup's waves (four or eight) share a tile of 16 NT WR rows: WR waves over
 // rows, the others over positions (interleaved steps).  A request's rows are cut
@@ -65,6 +67,7 @@ struct AttnPlan {
   int nt;           // 16-row tiles per wave
   bool ring;        // waves share keys and values through LDS
   int row_blocks;   // 16-row blocks of a part that may hold rows
+  bool whole;       // tiles are not cut
   size_t cut_bytes, ml_bytes, o_bytes;   // workspace: AttnCut[groups], (m, l), O
 };
 AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64_t capacity);
@@ -199,25 +202,12 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The hardware's maximum as it is (the compiler's would make signalling NaN quiet
-// first); a NaN operand loses against a number.
-__device__ __forceinline__ float max2(float x, float y) {
-  float r;
-  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
-  return r;
-}
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
-  return r;
-}
-
 // Over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false);
-  x = max2(as_float(a[0]), as_float(a[1]));
+  x = fmaxf(as_float(a[0]), as_float(a[1]));
   const auto b = __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false);
-  return max2(as_float(b[0]), as_float(b[1]));
+  return fmaxf(as_float(b[0]), as_float(b[1]));
 }
 __device__ __forceinline__ float groups_sum(float x) {
   x += __shfl_xor(x, 16);
@@ -245,7 +235,7 @@ __device__ __forceinline__ int tile_cost(int unit) {
   return unit < kTileCost ? kTileCost / unit : 1;
 }
 template <int NT, int TOK, int WAVES, bool RING>
-__device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) {
+__device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group, bool whole) {
   Req q;
   const int64_t s = a.cu[r], e = a.cu[r + 1];
   const int64_t n = s < 0 || e < s ? 0 : e - s;
@@ -269,6 +259,10 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group) 
   q.units_full = tile_cost(TOK) + steps;
   const int wt = q.wr_last ? WAVES / q.wr_last : 1;
   q.units_last = q.wr_last ? tile_cost(TOK * wt) + (steps + wt - 1) / wt : 0;
+  if (whole) {
+    q.units_full = 1;
+    q.units_last = q.wr_last ? 1 : 0;
+  }
   return q;
 }
 
@@ -285,8 +279,8 @@ constexpr int attn_waves(int nt, int d, bool ring) {
 // Launch with kThreads threads; a run of units per workgroup.
 template <int DT, bool F8, int D, int NT, int kPage, bool kRing>
 __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)) void tree_attention_kernel(
-    const TreeAttnArgs a, AttnCut* __restrict__ cuts, float* __restrict__ part_ml,
-    float* __restrict__ part_o) {
+    const TreeAttnArgs a, const bool whole, AttnCut* __restrict__ cuts,
+    float* __restrict__ part_ml, float* __restrict__ part_o) {
   constexpr int kWaves = attn_group(D, kRing);
   constexpr int kThreads = 64 * kWaves;
   constexpr int kC = F8 ? 16 : 8;        // positions of a lane's 16 bytes of values
@@ -335,7 +329,7 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     const int per = (a.R + kThreads - 1) / kThreads;
     const int r0 = min(t * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group).head_units();
+    for (int r = r0; r < r1; ++r) mine += a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group, whole).head_units();
     int64_t inc = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -357,7 +351,7 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     int64_t first = pre + inc - mine;
     if (w < w_end && w >= first && w < first + mine) {
       for (int r = r0; r < r1; ++r) {
-        const int64_t u = a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group).head_units();
+        const int64_t u = a.Hk * request<NT, kTok, kWaves, kRing>(a, r, group, whole).head_units();
         if (w < first + u) {
           sh_pos[0] = r;
           sh_pos[1] = w - first;
@@ -369,12 +363,12 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     __syncthreads();
   }
   if (w >= w_end) {
-    if (t == 0) cuts[b] = AttnCut{0, 0, 0, 0, 0, 0};
+    if (t == 0 && !whole) cuts[b] = AttnCut{0, 0, 0, 0, 0, 0};
     return;
   }
   int r = uni((int)sh_pos[0]);
   AttnCut cut = {0, 0, 0, 0, 0, 0};
-  Req rq = request<NT, kTok, kWaves, kRing>(a, r, group);
+  Req rq = request<NT, kTok, kWaves, kRing>(a, r, group, whole);
   // the first tile by division, the others by counting
   int h, row_tile, s0;
   {
@@ -452,14 +446,16 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     bool bad = rq.bad;
     const int t_step = kTok * wt;
     const int cost = tile_cost(t_step);
-    int t0 = uni((max(s0 - cost, 0) * wt + my_t) * kTok);
-    const int t_end = uni(idle || bad ? 0 : min(seen, (s1 - cost) * t_step));
+    const int from = whole ? 0 : max(s0 - cost, 0) * wt * kTok;
+    const int to = whole ? total : (s1 - cost) * t_step;
+    int t0 = uni(from + my_t * kTok);
+    const int t_end = uni(idle || bad ? 0 : min(seen, to));
     // the same of the whole tile: waves that share a ring take part to its end
-    const int t0_tile = max(s0 - cost, 0) * wt * kTok;
+    const int t0_tile = from;
     int seen_tile = total;
     if (!a.mask)
       seen_tile = min(seen_tile, ctx + (min(rq.rows, (row_tile * kWaves + wr) * 16 * NT) - 1) / group + 1);
-    const int t_end_tile = uni(bad ? 0 : min(seen_tile, (s1 - cost) * t_step));
+    const int t_end_tile = uni(bad ? 0 : min(seen_tile, to));
 
     if (kRing ? t0_tile < t_end_tile : t0 < t_end) {
       const int shift = kPage ? kPage : a.shift;
@@ -666,11 +662,11 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
         bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float x = max2(s[nt][0][0], s[nt][0][1]);
-          x = max3(x, s[nt][0][2], s[nt][0][3]);
+          float x = s[nt][0][0];
 #pragma unroll
-          for (int kt = 1; kt < kKT; ++kt)
-            x = max3(max3(x, s[nt][kt][0], s[nt][kt][1]), s[nt][kt][2], s[nt][kt][3]);
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x = fmaxf(x, s[nt][kt][i]);
           top[nt] = groups_max(x) * sc;
           rise |= top[nt] > m[nt] + kSlack;
         }
@@ -896,14 +892,14 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     }
 
     // ---- out ----
-    const bool whole = s0 == 0 && s1 == units;
+    const bool complete = s0 == 0 && s1 == units;
     if (my_t == 0) {
       const float vs = a.v_scale ? a.v_scale[h] : 1.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int row = row0 + nt * 16 + col;
         const float sum = groups_sum(l[nt]);
-        if (whole) {
+        if (complete) {
           if (row < rq.rows) {
             const int y = h * group + row - el[nt] * group;
             const float f = sum == 0.0f ? 0.0f : vs / sum;
@@ -931,7 +927,7 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
         }
       }
     }
-    if (!whole && s0 == 0) {
+    if (!complete && s0 == 0) {
       // the tile's last unit belongs to the workgroup that ends the row of parts
       const int64_t last = w + (units - 1);
       int64_t owner = last * runs / all;
@@ -953,11 +949,11 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
     }
     if (h >= a.Hk) {
       h = 0;
-      do rq = request<NT, kTok, kWaves, kRing>(a, ++r, group);
+      do rq = request<NT, kTok, kWaves, kRing>(a, ++r, group, whole);
       while (rq.rows == 0);                // there is one: units are left
     }
   }
-  if (t == 0) cuts[b] = cut;
+  if (t == 0 && !whole) cuts[b] = cut;
 }
 
 // Joins the parts of cut tiles.  Grid: (workgroups of the first launch, 16-row
@@ -1040,9 +1036,9 @@ dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
                 : F8 && a.shift == 5 ? &tree_attention_kernel<DT, F8, D, NT, F8 ? 5 : 0, RING>
                                      : &tree_attention_kernel<DT, F8, D, NT, 0, RING>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)p.groups), dim3(64 * attn_group(D, RING)), 0, stream, a,
-                     cuts, ml, po);
+                     p.whole, cuts, ml, po);
   const dspark_status st = check_launch("tree_attention_kernel");
-  if (st != DSPARK_OK) return st;
+  if (st != DSPARK_OK || p.whole) return st;
   hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, attn_group(D, RING) * NT>),
                      dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kJoinThreads), 0, stream, a,
                      cuts, ml, po);

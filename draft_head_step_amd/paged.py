@@ -20,69 +20,66 @@ _CACHE = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
 
 def _gpu(t, name):
-    if not t.is_cuda:
+    """Index of the device that a tensor is on."""
+    i = t.get_device()
+    if i < 0:
         raise ValueError(f"{name} must be a device tensor, got {t.device}")
-    return t.device
+    return i
 
 
 def _arr(t, name, dtype, shape, device):
-    """A dense tensor of that dtype, shape and device."""
+    """A dense tensor of that dtype, shape and device (index)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, dtypes, shape, device):
-    """[N, H, D] rows: dense heads, any row stride."""
+    """[N, H, D] rows: dense heads, any row stride, which is returned."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must have dtype in {tuple(dtypes)}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, got {t.device}")
     n, h, d = t.stride()
     if (d != 1 and shape[2] > 1) or (h != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must have dense rows of [heads, D]")
     # a single row has no row stride of its own
-    return n if shape[0] > 1 else max(n, shape[1] * shape[2]) if n % 8 == 0 else shape[1] * shape[2]
+    return n if shape[0] > 1 else shape[1] * shape[2]
 
 
 class _Call:
-    """The stream a call enqueues on, with its tensors' device current meanwhile."""
+    """The stream a call enqueues on, with the device of its tensors (an index) current
+    meanwhile and its own allocations on that stream."""
 
-    __slots__ = ("stream", "device", "back", "ctx")
+    __slots__ = ("stream", "device", "contexts")
 
     def __init__(self, device, stream):
         self.stream = stream
         self.device = device
+        self.contexts = ()
 
     def __enter__(self):
-        self.back = None
-        self.ctx = None
-        i = self.device.index
-        if i != torch.cuda.current_device():
-            self.back = torch.cuda.device(i)
-            self.back.__enter__()
-        if self.stream is None:
+        i, s = self.device, self.stream
+        if s is None and i == torch._C._cuda_getDevice():
             return torch._C._cuda_getCurrentRawStream(i)
-        if self.stream.device.index != i:
-            if self.back is not None:
-                self.back.__exit__(None, None, None)
-            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors are on {self.device}")
-        self.ctx = torch.cuda.stream(self.stream)
-        self.ctx.__enter__()
-        return self.stream.cuda_stream
+        if s is not None and s.device.index != i:
+            raise ValueError(f"the stream belongs to {s.device}, the tensors are on device {i}")
+        self.contexts = (torch.cuda.device(i),) if s is None else (torch.cuda.device(i), torch.cuda.stream(s))
+        for c in self.contexts:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(i)
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        if self.back is not None:
-            self.back.__exit__(*exc)
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
         return False
 
 
@@ -115,15 +112,15 @@ def dspark_page_map(cur_len, cu_seqlens, block_table, ring, pool, page_size, max
         raise ValueError("max_tokens or slots must be given")
     with _Call(dev, stream) as s:
         if slots is None:
-            slots = torch.empty((max_tokens,), dtype=torch.int64, device=dev)
+            slots = cur_len.new_empty((max_tokens,), dtype=torch.int64)
         if new_len is None:
-            new_len = torch.empty((R,), dtype=_I32, device=dev)
+            new_len = cur_len.new_empty((R,), dtype=_I32)
         if pool_out is None:
-            pool_out = torch.empty((4,), dtype=_I32, device=dev)
+            pool_out = cur_len.new_empty((4,), dtype=_I32)
         _arr(slots, "slots", torch.int64, (max_tokens,), dev)
         _arr(new_len, "new_len", _I32, (R,), dev)
         _pool(pool_out, "pool_out", dev)
-        st = _D.lib().dspark_page_map(
+        st = (_D._LIB or _D.lib()).dspark_page_map(
             cur_len.data_ptr(), cu_seqlens.data_ptr(), R, max_tokens, page_size, mp, ring.numel(),
             block_table.data_ptr(), ring.data_ptr(), pool.data_ptr(), pool_out.data_ptr(),
             slots.data_ptr(), new_len.data_ptr(), s)
@@ -148,9 +145,9 @@ def dspark_page_trim(cur_len, keep_len, block_table, ring, pool, page_size, *, p
     _pool(pool, "pool", dev)
     with _Call(dev, stream) as s:
         if pool_out is None:
-            pool_out = torch.empty((4,), dtype=_I32, device=dev)
+            pool_out = cur_len.new_empty((4,), dtype=_I32)
         _pool(pool_out, "pool_out", dev)
-        st = _D.lib().dspark_page_trim(
+        st = (_D._LIB or _D.lib()).dspark_page_trim(
             cur_len.data_ptr(), keep_len.data_ptr(), R, page_size, mp, ring.numel(),
             block_table.data_ptr(), ring.data_ptr(), pool.data_ptr(), pool_out.data_ptr(), s)
     if st:
@@ -169,7 +166,7 @@ def _cache_shape(k_cache, v_cache, lead=0):
     if k_cache.shape[lead:] != (n, hk, d // c, p, c) or k_cache.shape[:lead] != v_cache.shape[:lead]:
         raise ValueError(f"k_cache must be {(n, hk, d // c, p, c)} for v_cache {(n, hk, d, p)}, got "
                          f"{tuple(k_cache.shape)}")
-    if v_cache.device != k_cache.device:
+    if v_cache.get_device() != k_cache.get_device():
         raise ValueError("k_cache and v_cache must be on one device")
     return n, hk, d, p
 
@@ -198,8 +195,8 @@ def dspark_kv_store(k, v, slots, k_cache, v_cache, *, count=None, k_scale=None, 
     n, hk, d, p = _cache_shape(k_cache, v_cache)
     _dense(k_cache, "k_cache")
     _dense(v_cache, "v_cache")
-    if k_cache.device != dev:
-        raise ValueError(f"the caches must be on {dev}, got {k_cache.device}")
+    if k_cache.get_device() != dev:
+        raise ValueError(f"the caches must be on device {dev}, got {k_cache.device}")
     N = slots.numel()
     ks = _rows(k, "k", (torch.bfloat16, torch.float16), (N, hk, d), dev)
     vs = _rows(v, "v", (k.dtype,), (N, hk, d), dev)
@@ -208,7 +205,7 @@ def dspark_kv_store(k, v, slots, k_cache, v_cache, *, count=None, k_scale=None, 
         _arr(count, "count", _I32, (1,), dev)
     sk, sv = _scales(k_cache, k_scale, v_scale, hk, dev)
     with _Call(dev, stream) as s:
-        st = _D.lib().dspark_kv_store(
+        st = (_D._LIB or _D.lib()).dspark_kv_store(
             k.data_ptr(), v.data_ptr(), ks, vs, _CACHE[k.dtype], slots.data_ptr(),
             0 if count is None else count.data_ptr(), N, hk, d, p, n, _CACHE[k_cache.dtype], sk,
             sv, k_cache.data_ptr(), v_cache.data_ptr(), s)
@@ -247,9 +244,9 @@ def dspark_kv_commit(k_cache, v_cache, block_table, ctx_len, path, accepted, *, 
     _arr(accepted, "accepted", _I32, (R,), dev)
     with _Call(dev, stream) as s:
         if new_len is None:
-            new_len = torch.empty((R,), dtype=_I32, device=dev)
+            new_len = ctx_len.new_empty((R,), dtype=_I32)
         _arr(new_len, "new_len", _I32, (R,), dev)
-        st = _D.lib().dspark_kv_commit(
+        st = (_D._LIB or _D.lib()).dspark_kv_commit(
             k_cache.data_ptr(), v_cache.data_ptr(), kl, vl, layers, _CACHE[k_cache.dtype],
             block_table.data_ptr(), ctx_len.data_ptr(), path.data_ptr(), accepted.data_ptr(), R,
             nodes, hk, d, p, mp, n, new_len.data_ptr(), s)
@@ -259,7 +256,7 @@ def dspark_kv_commit(k_cache, v_cache, block_table, ctx_len, path, accepted, *, 
 
 
 def dspark_tree_attention_workspace(R: int, max_tokens: int, Hq: int, Hk: int, D: int) -> int:
-    return int(_D.lib().dspark_tree_attention_workspace(R, max_tokens, Hq, Hk, D))
+    return int((_D._LIB or _D.lib()).dspark_tree_attention_workspace(R, max_tokens, Hq, Hk, D))
 
 
 def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens, scale=None, *,
@@ -274,8 +271,8 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens,
     n, hk, d, p = _cache_shape(k_cache, v_cache)
     _dense(k_cache, "k_cache")
     _dense(v_cache, "v_cache")
-    if k_cache.device != dev:
-        raise ValueError(f"the caches must be on {dev}, got {k_cache.device}")
+    if k_cache.get_device() != dev:
+        raise ValueError(f"the caches must be on device {dev}, got {k_cache.device}")
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [N, Hq, D] and block_table [R, max_pages]")
     N, hq = q.shape[0], q.shape[1]
@@ -290,22 +287,22 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens,
         _arr(tree_mask, "tree_mask", torch.uint32 if tree_mask.dtype == torch.uint32 else _I32,
              (N, words), dev)
     sk, sv = _scales(k_cache, k_scale, v_scale, hk, dev)
-    L = _D.lib()
+    L = _D._LIB or _D.lib()
     with _Call(dev, stream) as s:
         if out is None:
-            out = torch.empty((N, hq, d), dtype=q.dtype, device=dev)
+            out = q.new_empty((N, hq, d), dtype=q.dtype)
             os_ = hq * d
         else:
             os_ = _rows(out, "out", (q.dtype,), (N, hq, d), dev)
         if lse is None and want_lse:
-            lse = torch.empty((N, hq), dtype=_F32, device=dev)
+            lse = q.new_empty((N, hq), dtype=_F32)
         elif lse is not None:
             _arr(lse, "lse", _F32, (N, hq), dev)
         if workspace is None:
             need = L.dspark_tree_attention_workspace(R, N, hq, hk, d)
-            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+            workspace = q.new_empty((max(need, 1),), dtype=torch.uint8)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
         st = L.dspark_tree_attention(
             q.data_ptr(), qs, _CACHE[q.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
             _CACHE[k_cache.dtype], sk, sv, block_table.data_ptr(), ctx_len.data_ptr(),
@@ -332,16 +329,16 @@ def dspark_tree_pack(parents, cu_seqlens, mask_words, pos0=None, *, mask=None, f
         _arr(pos0, "pos0", _I32, (R,), dev)
     with _Call(dev, stream) as s:
         if mask is None:
-            mask = torch.empty((N, mask_words), dtype=_I32, device=dev)
+            mask = parents.new_empty((N, mask_words), dtype=_I32)
         if flat_pos is None and want_pos:
-            flat_pos = torch.empty((N,), dtype=_I32, device=dev)
+            flat_pos = parents.new_empty((N,), dtype=_I32)
         if flat_req is None and want_req:
-            flat_req = torch.empty((N,), dtype=_I32, device=dev)
+            flat_req = parents.new_empty((N,), dtype=_I32)
         _arr(mask, "mask", torch.uint32 if mask.dtype == torch.uint32 else _I32, (N, mask_words), dev)
         for t, name in ((flat_pos, "flat_pos"), (flat_req, "flat_req")):
             if t is not None:
                 _arr(t, name, _I32, (N,), dev)
-        st = _D.lib().dspark_tree_pack(
+        st = (_D._LIB or _D.lib()).dspark_tree_pack(
             parents.data_ptr(), cu_seqlens.data_ptr(), 0 if pos0 is None else pos0.data_ptr(), R, N,
             mask_words, mask.data_ptr(), 0 if flat_pos is None else flat_pos.data_ptr(),
             0 if flat_req is None else flat_req.data_ptr(), s)
@@ -367,18 +364,18 @@ def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *,
     _arr(target_logits, "target_logits", _F32, (N, V), dev)
     with _Call(dev, stream) as s:
         if target_argmax is None:
-            target_argmax = torch.empty((N,), dtype=_I32, device=dev)
+            target_argmax = tokens.new_empty((N,), dtype=_I32)
         if accepted is None:
-            accepted = torch.empty((R,), dtype=_I32, device=dev)
+            accepted = tokens.new_empty((R,), dtype=_I32)
         if path is None:
-            path = torch.empty((R, max_nodes), dtype=_I32, device=dev)
+            path = tokens.new_empty((R, max_nodes), dtype=_I32)
         if next_token is None:
-            next_token = torch.empty((R,), dtype=_I32, device=dev)
+            next_token = tokens.new_empty((R,), dtype=_I32)
         _arr(target_argmax, "target_argmax", _I32, (N,), dev)
         _arr(accepted, "accepted", _I32, (R,), dev)
         _arr(path, "path", _I32, (R, max_nodes), dev)
         _arr(next_token, "next_token", _I32, (R,), dev)
-        st = _D.lib().dspark_verify_tree(
+        st = (_D._LIB or _D.lib()).dspark_verify_tree(
             target_logits.data_ptr(), cu_seqlens.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
             R, N, max_nodes, V, target_argmax.data_ptr(), accepted.data_ptr(), path.data_ptr(),
             next_token.data_ptr(), s)
