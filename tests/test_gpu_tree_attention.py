@@ -156,6 +156,97 @@ def test_long_context_split_and_joined(tree):
     check(c, out, lse)
 
 
+@pytest.mark.parametrize("Dh", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("P", [16, 32, 64, 256])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+def test_many_rows_over_a_cut_context(Dh, P, dtype, cache):
+    # tiles of all waves and of some, cut between workgroups, in every head size and page kind
+    print(f"case attention many rows D={Dh} P={P} {dtype} {cache}", flush=True)
+    c = make(300 + Dh + P, [70, 3, 33], [1500, 2100, 640], 8, 2, Dh, P, dtype, cache, tree=P != 32)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [[5, 2, 4], [40, 30, 50]])
+def test_long_masks(n, cache):
+    # mask rows of more than two words, for few rows and for many, around an odd start
+    print(f"case attention long masks n={n} {cache}", flush=True)
+    c = make(310, n, [45, 700, 131], 4, 2, 128, 16, "bf16", cache, tree=True, words=6)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+    c = make(311, [150, 97], [77, 3], 2, 1, 64, 64, "bf16", cache, tree=True)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+
+
+def test_hundreds_of_requests():
+    # more requests than threads scan their lengths
+    print("case attention 700 requests", flush=True)
+    rng = np.random.default_rng(9)
+    c = make(312, rng.integers(0, 4, 700), rng.integers(0, 60, 700), 2, 1, 64, 16)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+    c = make(313, rng.integers(0, 3, 600), rng.integers(0, 600, 600), 2, 2, 64, 32)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11])
+def test_scales_without_a_usual_sign(scale):
+    print(f"case attention scale {scale}", flush=True)
+    for tree in (False, True):
+        c = make(314, [5, 40], [70, 600], 8, 2, 64, 16, tree=tree)
+        c["scale"] = scale
+        out, lse = call(c, want_lse=True)
+        torch.cuda.synchronize()
+        check(c, out, lse)
+
+
+def test_binding_refuses_what_does_not_fit():
+    print("case attention refusals", flush=True)
+    c = make(315, [3, 2], [20, 5], 4, 2, 64, 16)
+    f = make(315, [3, 2], [20, 5], 4, 2, 64, 16, cache="e4m3")
+
+    def bad(error, base=c, **kw):
+        d = dict(base)
+        d.update(kw)
+        with pytest.raises(error):
+            call(d)
+
+    bad(ValueError, table=c["table"][:1])
+    bad(TypeError, table=c["table"].astype(np.int64))
+    bad(ValueError, ctx=c["ctx"][:1])
+    bad(ValueError, cu=c["cu"][:2])
+    bad(TypeError, q=c["q"].float())
+    bad(ValueError, q=c["q"].transpose(0, 1))
+    bad(ValueError, q=c["q"][:, :, :32])
+    bad(TypeError, vc=c["vc"].half())
+    bad(ValueError, vc=c["vc"][:-1])
+    bad(ValueError, kc=c["kc"].transpose(2, 3))
+    bad(ValueError, mask=np.zeros((3, 1), np.uint32))
+    bad(D.DsparkError, q=c["q"][:, :3].contiguous())             # heads no multiple of the caches'
+    bad(D.DsparkError, q=c["q"].half())                          # another type than the cache's
+    bad(D.DsparkError, base=f, ks=None, vs=None)                 # no scales
+    bad(D.DsparkError, ks=np.ones(2, np.float32), vs=np.ones(2, np.float32))
+    bad(ValueError, base=f, vs=None)
+    bad(D.DsparkError, scale=float("nan"))
+    bad(D.DsparkError, q=c["q"][:1].expand(5, 4, 64))            # rows that lie on each other
+    with pytest.raises(D.DsparkError):
+        call(c, workspace=torch.empty(512, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        call(c, workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        call(c, out=torch.empty((5, 4, 32), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(TypeError):
+        call(c, lse=torch.empty((5, 4), dtype=torch.float16, device=DEV))
+
+
 def test_rows_that_see_nothing():
     # mask rows of zeros: without a context nothing is seen, with one the context alone
     print("case attention empty rows", flush=True)
