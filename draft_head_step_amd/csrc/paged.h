@@ -16,6 +16,7 @@ namespace dspark {
 
 constexpr int kMinPage = 16;
 constexpr int kMaxPage = 1024;
+constexpr int64_t kMaxLen = 0x7fffffff;   // of a request, kept as int32
 
 // log2 of a page size, -1 if it is not a power of two in [16, 1024].
 DSPARK_HD int page_shift(int page_size) {
@@ -38,7 +39,8 @@ DSPARK_HD bool slot_ok(int64_t slot, int shift, int num_pages) {
 }
 
 // What dspark_page_map does for one request: the pages that it has and wants,
-// and whether its lengths fit (otherwise it asks for nothing).
+// and whether its lengths fit, into the table and into an int32 (otherwise it
+// asks for nothing).
 struct PageNeed {
   int64_t has, want;
   bool fits;
@@ -49,7 +51,7 @@ DSPARK_HD PageNeed page_need(int32_t cur, int32_t first, int32_t end, int shift,
   p.fits = cur >= 0 && n >= 0 && first >= 0;
   p.has = p.fits ? pages_of(cur, shift) : 0;
   p.want = p.fits ? pages_of((int64_t)cur + n, shift) : 0;
-  p.fits = p.fits && p.want <= max_pages;
+  p.fits = p.fits && p.want <= max_pages && cur + n <= kMaxLen;
   return p;
 }
 

@@ -5,7 +5,8 @@
 // parent's number is smaller than its child's, so a walk meets the bits from
 // the highest word down and a row is written word by word with no array of
 // words in registers.  Bound by the length of the longest chain (about 64
-// cycles of LDS latency a step).
+// cycles of LDS latency a step): 2.3 us for 4 small trees, 3 to 4.6 for 32 trees of
+// up to 64 nodes.
 #include "dspark_internal.h"
 #include "paged.h"
 

@@ -231,6 +231,8 @@ __global__ __launch_bounds__(kRowT) void verify_argmax_kernel(const float* __res
 // the lowest-numbered one behind it (a child's number is larger than its
 // parent's) whose parent is `at` and whose token is the target's after `at`:
 // 64 nodes are tried at a time, the lowest set bit of the wave's vote is taken.
+// Bound by the dependent reads of a path's nodes: 4.7 us for 32 trees of up to 64
+// nodes, behind 99 us for the argmaxes of their 1188 rows of 129280 (6.2 TB/s).
 __global__ __launch_bounds__(64) void verify_walk_kernel(
     const int32_t* __restrict__ amax, const int32_t* __restrict__ cu,
     const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents, int max_tokens,

@@ -468,6 +468,9 @@ dspark_status dspark_accept_prob(const float* draft_logits, const float* target_
  * either feeds them without a transpose.  DSPARK_E4M3 caches hold x / scale in
  * OCP e4m3 (finite values up to 448) with one scale per head for the keys and
  * one for the values.
+ *
+ * Outputs share no memory with inputs or with each other unless an entry says
+ * that they may.
  * ------------------------------------------------------------------------ */
 
 /* Element types of the cache calls. */
@@ -499,7 +502,8 @@ typedef struct {
  *     block_table[r, ceil(cur_len[r] / P) + i] = ring[(head + S_r + i) mod num_pages]
  * slots[cu_seqlens[r] + j] is the slot of position cur_len[r] + j and
  * new_len[r] = cur_len[r] + n_r.  A request that is not served (the pool is
- * short, cur_len[r] or n_r negative, or more than max_pages pages) leaves its
+ * short, cur_len[r] or n_r negative, more than max_pages pages or 2^31 - 1 tokens)
+ * leaves its
  * block_table row as it was, gets slots of -1 and new_len[r] = cur_len[r], and
  * counts in pool_out->refused; one that asks for no page is served whatever
  * the pool holds, and one with too many pages takes none from the others.  A
@@ -509,13 +513,13 @@ typedef struct {
  *   block_table [R, max_pages] int32, new entries written.
  *   ring        [num_pages] int32 (read).
  *   pool        device dspark_page_pool before the call (read).
- *   pool_out    device dspark_page_pool after it; another address than pool, so
- *               that a call can be repeated.
+ *   pool_out    device dspark_page_pool after it; apart from pool, so that a call
+ *               can be repeated.
  *   slots       [max_tokens] int64 output; entries from cu_seqlens[R] on are left
  *               as they were, elements from max_tokens on get no slot.
- *   new_len     [R] int32 output; another address than cur_len.
+ *   new_len     [R] int32 output, apart from cur_len.
  * One launch.  Errors: EINVAL for NULL pointers, sizes <= 0, a page size that
- * is no power of two in [16, 1024], pool_out == pool or new_len == cur_len;
+ * is no power of two in [16, 1024], pool_out on pool or new_len on cur_len;
  * EUNSUPPORTED for R > DSPARK_MAX_PAGE_REQUESTS; EDEVICE on a launch failure.
  */
 dspark_status dspark_page_map(const int32_t* cur_len, const int32_t* cu_seqlens, int R,
@@ -578,9 +582,10 @@ dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, in
  *               dspark_verify_tree writes them).
  * A request whose path is not such a sequence, whose accepted count lies
  * outside [-1, max_nodes), or that touches a page id outside [0, num_pages) or
- * a position past its table moves nothing and gets new_len[r] = -1.
+ * a position past its table or 2^31 - 1 moves nothing and gets new_len[r] = -1.
+ *   new_len     [R] int32 output, apart from ctx_len and accepted.
  * Errors: EINVAL for NULL pointers, sizes <= 0, a bad page size or type,
- * misaligned caches or strides; EUNSUPPORTED for D as above, layers > 65535 or
+ * misaligned caches or strides, new_len on ctx_len or accepted; EUNSUPPORTED for D as above, layers > 65535 or
  * R > 65535; EDEVICE.
  */
 dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
@@ -615,14 +620,16 @@ size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, in
  *               min(cu_seqlens[R], max_tokens) on are neither read nor written.
  *   tree_mask   [max_tokens, mask_words] uint32 or NULL (mask_words is then 0).
  *   k_scale, v_scale  [Hk] fp32 with a DSPARK_E4M3 cache, NULL otherwise.
- *   scale       finite.
- *   out         rows of [Hq, D] elements of `dtype`, row e at out + e * out_stride.
+ *   scale       finite, also times log2(e).
+ *   out         rows of [Hq, D] elements of `dtype`, row e at out + e * out_stride;
+ *               may be q itself, with its stride.
  *   lse         optional [max_tokens, Hq] fp32.
  *   workspace   >= dspark_tree_attention_workspace(...) bytes, 256-byte aligned;
- *               its contents on entry do not matter.
+ *               its contents on entry do not matter, and calls that may run at
+ *               the same time need one each.
  * A request's rows are NaN where ctx_len[r] < 0 or it has more positions than its
- * table, and rows that read a page id outside [0, num_pages) are NaN (rows of
- * a chain need not read the pages behind them).
+ * table (or 2^31 - 2^16).  A page id outside [0, num_pages) is not touched: rows
+ * that see a position of it are NaN, and other rows of the request may be.
  * Where a row's sums are split depends on the lengths of the whole batch: the
  * same call gives the same bits, a request in another batch the same values up
  * to the rounding of fp32 sums.

@@ -27,7 +27,7 @@ def page_map(cur, cu, table, ring, pool, P, max_tokens, slots):
     new_len = cur.copy()
     for r in range(R):
         n = int(cu[r + 1] - cu[r])
-        fits = cur[r] >= 0 and n >= 0 and _up(cur[r] + n, P) <= width
+        fits = cur[r] >= 0 and n >= 0 and _up(cur[r] + n, P) <= width and cur[r] + n < 2 ** 31
         has = _up(cur[r], P) if fits else 0
         need = _up(cur[r] + n, P) - has if fits else 0
         served = fits and (need == 0 or asked + need <= count)

@@ -380,3 +380,21 @@ def test_verify_tree_of_chains_equals_verify_greedy():
     assert torch.equal(acc, acc2) and torch.equal(nxt, nxt2) and torch.equal(top[:N], top2)
     for r in range(50):
         assert path[r].tolist() == list(range(int(acc[r]) + 1)) + [-1] * (5 - int(acc[r]))
+
+
+def test_lengths_beyond_an_int32_are_refused():
+    print("case lengths at 2^31", flush=True)
+    top, P, width = 2 ** 31 - 1, 1024, (1 << 21) + 4
+    table = torch.zeros((2, width), dtype=torch.int32, device=DEV)
+    cur = dev(np.array([top - 2, 5], np.int32))
+    cu = dev(np.array([0, 4, 6], np.int32))
+    ring = dev(np.arange(8, dtype=np.int32))
+    pool = dev(np.array([0, 8, 0, 0], np.int32))
+    slots, new, after = D.dspark_page_map(cur, cu, table, ring, pool, P, 6)
+    assert new.tolist() == [top - 2, 7] and after.tolist() == [0, 8, 1, 0]
+    assert slots.tolist() == [-1] * 4 + [5, 6]
+    kc = torch.zeros((8, 1, 8, P, 8), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros((8, 1, 64, P), dtype=torch.bfloat16, device=DEV)
+    path = dev(np.array([[0, 2, 3, -1], [0, 1, -1, -1]], np.int32))
+    new = D.dspark_kv_commit(kc, vc, table, cur, path, dev(np.array([2, 1], np.int32)))
+    assert new.tolist() == [-1, 7]

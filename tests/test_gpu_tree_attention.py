@@ -208,6 +208,20 @@ def test_scales_without_a_usual_sign(scale):
         check(c, out, lse)
 
 
+@pytest.mark.parametrize("n", [[1, 5, 3], [40, 9, 30]])
+def test_output_over_the_queries(n):
+    # the same rows as q: cut tiles and uncut ones, few rows and many
+    print(f"case attention in place n={n}", flush=True)
+    for ctx in ([3, 90, 20], [3000, 700, 1500]):
+        c = make(316, n, ctx, 8, 2, 128, 16)
+        want, _ = call(c)
+        c["q"] = c["q"].clone()
+        got, _ = call(c, out=c["q"])
+        torch.cuda.synchronize()
+        assert got.data_ptr() == c["q"].data_ptr()
+        assert torch.equal(got, want)
+
+
 def test_binding_refuses_what_does_not_fit():
     print("case attention refusals", flush=True)
     c = make(315, [3, 2], [20, 5], 4, 2, 64, 16)

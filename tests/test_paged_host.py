@@ -94,7 +94,7 @@ def test_page_needs(shim, shift):
             for mp in (1, 3, BIG):
                 has, want, fits = _three(shim.t_need, cur, a, b, shift, mp)
                 n = b - a
-                ok = cur >= 0 and n >= 0 and a >= 0 and -(-(cur + n) // size) <= mp
+                ok = cur >= 0 and n >= 0 and a >= 0 and -(-(cur + n) // size) <= mp and cur + n <= BIG
                 assert bool(fits) == ok
                 if ok:
                     assert (has, want) == (-(-cur // size), -(-(cur + n) // size))
@@ -148,7 +148,7 @@ def test_links_and_paths(shim):
     *[(dict([(n, None)]), EINVAL) for n in ("cur", "cu", "table", "ring", "pool", "out", "slots", "new")],
     (dict(R=0), EINVAL), (dict(N=0), EINVAL), (dict(mp=0), EINVAL), (dict(np_=-1), EINVAL),
     (dict(ps=8), EINVAL), (dict(ps=48), EINVAL), (dict(ps=2048), EINVAL), (dict(out=P), EINVAL),
-    (dict(new=2 * P), EINVAL), (dict(R=16385), EUNSUPPORTED),
+    (dict(new=2 * P), EINVAL), (dict(new=2 * P + 12), EINVAL), (dict(out=P + 8), EINVAL), (dict(R=16385), EUNSUPPORTED),
 ])
 def test_page_map_rejects(kw, want):
     a = dict(cur=2 * P, cu=P, R=4, N=8, ps=16, mp=4, np_=9, table=P, ring=P, pool=P, out=3 * P, slots=P, new=P)
@@ -194,7 +194,8 @@ def test_kv_store_rejects(kw, want):
     *[(dict([(n, 0)]), EINVAL) for n in ("L", "R", "nodes", "Hk", "D", "mp", "np_")],
     (dict(ct=3), EINVAL), (dict(ct=-1), EINVAL), (dict(ps=20), EINVAL), (dict(kl=4), EINVAL), (dict(vl=12), EINVAL),
     (dict(ct=2, kl=8), EINVAL), (dict(kc=P + 8), EINVAL), (dict(D=72), EUNSUPPORTED), (dict(L=70000), EUNSUPPORTED),
-    (dict(R=70000), EUNSUPPORTED),
+    (dict(R=70000), EUNSUPPORTED), (dict(new=P), EINVAL), (dict(ctx=2 * P, new=P + 4), EINVAL),
+    (dict(acc=2 * P, new=P - 4), EINVAL),
 ])
 def test_kv_commit_rejects(kw, want):
     a = dict(kc=P, vc=P, kl=0, vl=0, L=1, ct=0, table=P, ctx=P, path=P, acc=P, R=2, nodes=8, Hk=2, D=64, ps=16, mp=4, np_=9,
@@ -211,7 +212,7 @@ def test_kv_commit_rejects(kw, want):
     *[(dict([(n, 0)]), EINVAL) for n in ("R", "N", "Hq", "Hk", "D", "mp", "np_")],
     (dict(Hq=9), EINVAL), (dict(ps=12), EINVAL), (dict(dt=2), EINVAL), (dict(ct=1), EINVAL), (dict(ct=2), EINVAL),
     (dict(sk=P), EINVAL), (dict(words=1), EINVAL), (dict(mask=P, words=0), EINVAL), (dict(mask=P, words=-1), EINVAL),
-    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(q=P + 2), EINVAL), (dict(qs=516), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=3e38), EINVAL), (dict(q=P + 2), EINVAL), (dict(qs=516), EINVAL),
     (dict(qs=504), EINVAL), (dict(os=504), EINVAL), (dict(out=P + 8), EINVAL), (dict(D=48, qs=512), EUNSUPPORTED),
     (dict(mask=P, words=33), EUNSUPPORTED), (dict(R=(1 << 20) + 1), EUNSUPPORTED), (dict(N=1 << 29), EUNSUPPORTED),
     (dict(ws=None), EWORKSPACE), (dict(wb=16), EWORKSPACE), (dict(ws=P + 128), EINVAL),
