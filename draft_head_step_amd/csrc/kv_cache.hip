@@ -2,16 +2,15 @@
 //
 //   kv_store:  K and V rows of new elements into their slots.  The keys keep 16
 //              bytes (c elements) of a row together, [D / c][P][c]; the values
-//              lie transposed, [D][P].  A workgroup takes 32 elements of one
-//              head: rows are read 16 bytes a lane, pass through LDS, and are
+//              lie transposed, [D][P].  A workgroup takes 32 or 64 elements of
+//              one head: rows are read 16 bytes a lane, pass through LDS, and are
 //              written with neighbouring lanes on neighbouring elements, which
 //              in a run of slots are neighbouring addresses in both caches.
-//              18.8 thousand elements of 8 heads of 128 take 38 us in bf16 (4.1
-//              TB/s, a copy reaches 4.95) and 33 us in e4m3, where single bytes of
-//              the values go out and the divisions weigh.  16 elements a
-//              workgroup were 10 % slower at pages of 64, 64 elements 10 %
-//              slower for the 900 of a step; products with the reciprocal where
-//              both surely round alike gained nothing.
+//              The keys' stores are non-temporal (whole lines that nobody reads
+//              soon: 38 us, then 30); values share lines with other workgroups
+//              and are not.  18.8 thousand elements of 8 heads of 128 take 29 us
+//              in bf16 (5.4 TB/s, a copy of 2 GB reaches 4.95) and 26 us in e4m3
+//              (4.5 TB/s; 39 with a division for every value).
 //   kv_commit: the accepted path's keys and values to the front.  A thread
 //              owns 16-byte pieces of the keys and value channels and moves each
 //              for i = 1, 2, ... in turn, four positions' loads at a time.
@@ -33,7 +32,11 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kT = 256;
-constexpr int kTok = 32;   // elements per workgroup
+// Rows of one head from which a workgroup takes 64 elements: four workgroups a CU.
+// 64 instead of 32: 28.5 us and 29.7 for 151 thousand rows of 128 (pages of 64: 29.3
+// and 32.1; heads of 64: 12.8 and 15.4; of 256: 67 and 76, in e4m3 51 and 49), but
+// 9.1 and 8.4 for the 7 thousand of a step.
+constexpr int64_t kManyRows = 64 * 1024;
 
 __device__ __forceinline__ float widen(uint16_t x, bool bf) {
   return bf ? __builtin_bit_cast(float, (uint32_t)x << 16)
@@ -47,8 +50,53 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
   return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false);
 }
 
+// e4m3 of x / scale for eight values.  x times 1 / scale a little less and a little
+// more (2^-21: the reciprocal, its shift, the product and the quotient are each off
+// by 2^-24 at most) encloses the rounded quotient, and rounding to e4m3 is monotone:
+// where both ends round alike and stay in range that is the result, a fifth of the
+// instructions of a division.  Otherwise the division decides.
+struct Scale {
+  float s, low, high;
+  bool wide;   // the reciprocal is no normal number with room for the products
+};
+__device__ __forceinline__ Scale make_scale(float s) {
+  const float r = 1.0f / s;
+  return {s, r * (1.0f - 0x1p-21f), r * (1.0f + 0x1p-21f),
+          !(fabsf(r) >= 0x1p-100f && fabsf(r) <= 0x1p100f)};
+}
+__device__ __forceinline__ void eight_to_e4m3(u32x4 a, int bf, const Scale& sc, uint8_t* out) {
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = widen((uint16_t)(a[j >> 1] >> ((j & 1) * 16)), bf);
+  uint32_t lo[2], hi[2];
+  float top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float* y = x + 4 * w;
+    int l = 0, u = 0;
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * sc.low, y[1] * sc.low, l, false);
+    l = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * sc.low, y[3] * sc.low, l, true);
+    float z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z[j] = y[j] * sc.high;
+      top = fmaxf(top, fabsf(z[j]));
+    }
+    u = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], u, false);
+    u = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], u, true);
+    lo[w] = l;
+    hi[w] = u;
+  }
+  if (sc.wide || !(top <= 448.0f) || lo[0] != hi[0] || lo[1] != hi[1]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = to_e4m3(x[j] / sc.s);
+  } else {
+    __builtin_memcpy(out, lo, 8);
+  }
+}
+
 // Grid: (ceil(max_tokens / kTok), Hk).  F8: 8-bit cache of 16-bit inputs.
-template <int D, bool F8>
+template <int D, bool F8, int kTok>
 __global__ __launch_bounds__(kT) void kv_store_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride,
     int64_t v_stride, int bf, const int64_t* __restrict__ slots, const int32_t* __restrict__ count,
@@ -70,8 +118,8 @@ __global__ __launch_bounds__(kT) void kv_store_kernel(
   n = n - e0 < kTok ? n - e0 : kTok;
   if (n <= 0) return;
   if (t < kTok) slot[t] = t < n ? slots[e0 + t] : -1;
-  const float sk = F8 ? k_scale[h] : 1.0f;
-  const float sv = F8 ? v_scale[h] : 1.0f;
+  const Scale sk = make_scale(F8 ? k_scale[h] : 1.0f);
+  const Scale sv = make_scale(F8 ? v_scale[h] : 1.0f);
   constexpr int kPieces = D / 8;   // 16-byte pieces of an input row
   // all of a thread's loads before the first conversion
   constexpr int kLoads = (kTok * kPieces + kT - 1) / kT;
@@ -91,11 +139,8 @@ __global__ __launch_bounds__(kT) void kv_store_kernel(
     const u32x4 a = la[u], b = lb[u];
     if (F8) {
       uint8_t oa[8], ob[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        oa[j] = to_e4m3(widen((uint16_t)(a[j >> 1] >> ((j & 1) * 16)), bf) / sk);
-        ob[j] = to_e4m3(widen((uint16_t)(b[j >> 1] >> ((j & 1) * 16)), bf) / sv);
-      }
+      eight_to_e4m3(a, bf, sk, oa);
+      eight_to_e4m3(b, bf, sv, ob);
       __builtin_memcpy(&ks[e][p * 8], oa, 8);
       __builtin_memcpy(&vs[e][p * 8], ob, 8);
     } else {
@@ -110,8 +155,9 @@ __global__ __launch_bounds__(kT) void kv_store_kernel(
   const int64_t page = s >> shift;
   const int o = (int)(s & ((1 << shift) - 1));
   for (int p = t / kTok; p < D / kC; p += kT / kTok)
-    *reinterpret_cast<u32x4*>(k_cache + k_offset(page, h, p * kC, o, Hk, D, shift, kC) * kEl) =
-        *reinterpret_cast<const u32x4*>(&ks[e][p * 16]);
+    __builtin_nontemporal_store(
+        *reinterpret_cast<const u32x4*>(&ks[e][p * 16]),
+        reinterpret_cast<u32x4*>(k_cache + k_offset(page, h, p * kC, o, Hk, D, shift, kC) * kEl));
   for (int d = t / kTok; d < D; d += kT / kTok) {
     uint8_t* to = v_cache + v_offset(page, h, d, o, Hk, D, shift) * kEl;
     if (F8) *to = vs[e][d];
@@ -227,13 +273,18 @@ struct StoreArgs {
   uint8_t* v_cache;
 };
 
-template <int D>
-void store_d(bool f8, const StoreArgs& a, hipStream_t stream) {
-  auto kernel = f8 ? &kv_store_kernel<D, true> : &kv_store_kernel<D, false>;
+template <int D, int kTok>
+void store_tiles(bool f8, const StoreArgs& a, hipStream_t stream) {
+  auto kernel = f8 ? &kv_store_kernel<D, true, kTok> : &kv_store_kernel<D, false, kTok>;
   const dim3 grid((unsigned)(((int64_t)a.n + kTok - 1) / kTok), (unsigned)a.Hk);
   hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, stream, a.k, a.v, a.k_stride, a.v_stride, a.bf,
                      a.slots, a.count, a.n, a.Hk, a.shift, a.num_pages, a.k_scale, a.v_scale,
                      a.k_cache, a.v_cache);
+}
+template <int D>
+void store_d(bool f8, const StoreArgs& a, hipStream_t stream) {
+  if ((int64_t)a.n * a.Hk >= kManyRows) store_tiles<D, 64>(f8, a, stream);
+  else store_tiles<D, 32>(f8, a, stream);
 }
 
 }  // namespace

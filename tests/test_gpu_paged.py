@@ -239,6 +239,38 @@ def test_kv_store_rounds_every_value_to_the_nearest():
             assert np.array_equal(g[~nan], want[~nan]) and ((g[nan] & 127) == 127).all()
 
 
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("N,Hk,Dh,P", [(8201, 8, 64, 16), (5500, 12, 96, 64), (66000, 1, 128, 32), (4127, 16, 256, 16), (2100, 32, 192, 128)])
+def test_kv_store_of_many_elements(N, Hk, Dh, P, dtype, cache):
+    test_kv_store(N, Hk, Dh, P, dtype, cache, "run" if Dh % 64 else "mixed")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_kv_store_divides_by_any_scale(dtype):
+    # every value of the type by scales with exact ties, near ties, and none that a
+    # reciprocal could stand for; the quotient is fp32, rounded twice
+    print(f"case kv_store scales {dtype}", flush=True)
+    rng = np.random.default_rng(5)
+    scales = [1.0, 0.5, 2.0 ** -6, 3.0, 1 / 3, 0.1, 7.0, 1e-3, 448.0, 1e-30, 1e30, 1e-38, 3e38, 1e-40, 1e-45, 1.0000001, 0.99999994]
+    scales = np.array(scales + list(np.exp(rng.uniform(-20, 20, 15))), np.float32)
+    H = len(scales)
+    bits = torch.from_numpy(np.arange(65536, dtype=np.uint16).view(np.int16))
+    x = bits.view(torch.bfloat16 if dtype == "bf16" else torch.float16).reshape(512, 1, 128)
+    rows = x.expand(512, H, 128).contiguous().to(DEV)
+    kc = torch.zeros((32, H, 8, 16, 16), dtype=torch.float8_e4m3fn, device=DEV)
+    vc = torch.zeros((32, H, 128, 16), dtype=torch.float8_e4m3fn, device=DEV)
+    D.dspark_kv_store(rows, rows, torch.arange(512, device=DEV), kc, vc, k_scale=dev(scales), v_scale=dev(scales))
+    torch.cuda.synchronize()
+    k = _raw(kc).transpose(0, 3, 1, 2, 4).reshape(512, H, 128)
+    v = _raw(vc).transpose(0, 3, 1, 2).reshape(512, H, 128)
+    for i in range(H):
+        want = e4m3(x.float().numpy(), scales[i:i + 1])[:, 0]
+        nan = (want & 127) == 127
+        for g in (k[:, i], v[:, i]):
+            assert np.array_equal(g[~nan], want[~nan]), scales[i]
+            assert ((g[nan] & 127) == 127).all(), scales[i]
+
+
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("layers", [None, 3])
 @pytest.mark.parametrize("Hk,Dh,P", [(1, 64, 16), (3, 96, 32), (8, 128, 16)])
