@@ -50,7 +50,7 @@
 //   6 trees of 5 to 16 over 30 to 131 thousand positions, e4m3: 202 us for 1.03 GB,
 //     5.1 TB/s, with the widening of 8-bit operands beside it.
 //   24 trees of 33 to 64 over 1 to 6 thousand positions, 64 heads, fp16: 229 us for
-//     126 GFLOP, 550 TFLOP/s.  A step in the middle of a tile runs at 870 (a large
+//     126 GFLOP, 545 to 550 TFLOP/s.  A step in the middle of a tile runs at 870 (a large
 //     product at 1170), between the matrix cores and the exponentials; the rest is
 //     each tile's start and end, and the parts (64 MB out and in, 18 us to join).
 //   One token over 200 positions: 7.2 us, the latency of dependent loads.
