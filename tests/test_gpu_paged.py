@@ -111,6 +111,41 @@ def test_page_map_at_the_largest_request_count():
     assert e.value.status == 3
 
 
+def test_pages_of_many_requests_replay_in_a_graph():
+    # lengths that take more LDS than a kernel has without asking
+    print("case pages of 9000 requests in a graph", flush=True)
+    R, P, width = 9000, 16, 4
+    rng = np.random.default_rng(10)
+    cur, n = rng.integers(0, 40, R), rng.integers(0, 5, R)
+    cu = np.concatenate([[0], np.cumsum(n)])
+    N = int(cu[-1])
+    table, ring, pool = make_pool(rng, cur, P, width, 9000)
+    c, u, k = (dev(x.astype(np.int32)) for x in (cur, cu, cur // 2))
+    out = dict(table=dev(table), ring=dev(ring), slots=torch.zeros(N, dtype=torch.int64, device=DEV),
+               new=torch.zeros(R, dtype=torch.int32, device=DEV), a=dev(pool), b=dev(pool))
+    first = dev(pool)
+
+    def step(o):
+        D.dspark_page_map(c, u, o["table"], o["ring"], first, P, slots=o["slots"], new_len=o["new"], pool_out=o["a"])
+        D.dspark_page_trim(o["new"], k, o["table"], o["ring"], o["a"], P, pool_out=o["b"])
+
+    want = {x: t.clone() for x, t in out.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out)
+    step(want)
+    for _ in range(3):
+        out["slots"].zero_()
+        out["new"].zero_()
+        out["table"].copy_(dev(table))
+        out["ring"].copy_(dev(ring))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x in out:
+            assert torch.equal(out[x], want[x]), x
+
+
 def check_trim(cur, keep, table, ring, pool, P):
     r = dev(ring)
     out = D.dspark_page_trim(dev(cur), dev(keep), dev(table), r, dev(pool), P)
