@@ -49,6 +49,11 @@ AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64
   p.groups = (int)(groups < 1 ? 1 : groups);
   const int64_t blocks = ((int64_t)max_tokens * group + 15) / 16;
   p.row_blocks = (int)(blocks < waves * p.nt ? blocks : waves * p.nt);
+  // Eight workgroups for each tile that there is at least: its parts are joined by two
+  // waves (one request of 64 nodes over 8000 positions: 58 us, then 41; with four parts
+  // a tile, 16 chains, 45 and 46).
+  const int64_t row_tiles = blocks / (waves * p.nt);
+  p.deep = groups >= 8 * Hk * (row_tiles > R ? row_tiles : (int64_t)R);
   const size_t parts = (size_t)groups * 2 * waves * p.nt;
   p.cut_bytes = ((size_t)groups * sizeof(AttnCut) + 255) / 256 * 256;
   p.ml_bytes = parts * 2 * 64 * sizeof(float);

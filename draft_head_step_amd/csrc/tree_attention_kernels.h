@@ -79,6 +79,7 @@ struct AttnPlan {
   bool ring;        // waves share keys and values through LDS
   int row_blocks;   // 16-row blocks of a part that may hold rows
   bool whole;       // tiles are not cut
+  bool deep;        // a tile is likely to have many parts: two waves share a join
   size_t cut_bytes, ml_bytes, o_bytes;   // workspace: AttnCut[groups], (m, l), O
 };
 AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64_t capacity);
@@ -227,6 +228,12 @@ __device__ __forceinline__ float groups_sum(float x) {
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// The run of workgroup i of G: neighbouring runs on one XCD (workgroups go to the
+// eight XCDs in turn).
+__device__ __forceinline__ int run_of(int i, int G) {
+  return (G & 7) == 0 ? (i & 7) * (G >> 3) + (i >> 3) : i;
+}
+
 // A request as the work split sees it.
 struct Req {
   int start;        // its first element
@@ -328,13 +335,13 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
   const int g = lane >> 4;               // lane group
   const int group = a.Hq / a.Hk;
   const int G = gridDim.x;
-  // neighbouring runs on one XCD (workgroups go to the eight XCDs in turn)
-  const int b = (G & 7) == 0 ? (int)(blockIdx.x & 7) * (G >> 3) + (int)(blockIdx.x >> 3)
-                             : (int)blockIdx.x;
+  const int b = run_of(blockIdx.x, G);
 
   // ---- where this run starts ----
-  // With fewer units than workgroups each of the first ones takes one: every run
-  // between a tile's first and last part holds a part.
+  // With few units only the first workgroups take a run: every run between a tile's
+  // first and last part holds a part.  Runs of waves that share a ring have two units
+  // at least, their parts are as large as the keys and values of eight (2 trees of 20
+  // to 30 over 500 and 2000 positions: 33 us, then 30; four units gain no more).
   int64_t w, w_end, all, runs;
   {
     const int per = (a.R + kThreads - 1) / kThreads;
@@ -356,7 +363,8 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
       pre += j < wave ? sh_scan[j] : 0;
       all += sh_scan[j];
     }
-    runs = all < G ? all : G;
+    const int64_t most = kRing && !whole && all > 1 ? all / 2 : all;
+    runs = most < G ? most : G;
     w = b < runs ? all * b / runs : 0;
     w_end = b < runs ? all * (b + 1) / runs : 0;
     int64_t first = pre + inc - mine;
@@ -968,29 +976,37 @@ __global__ __launch_bounds__(64 * attn_group(D, kRing), attn_waves(NT, D, kRing)
 }
 
 // Joins the parts of cut tiles.  Grid: (workgroups of the first launch, 16-row
-// blocks of a tile).  Each of the four waves joins its share of the channels over
-// all parts, four parts' loads at a time; no wave waits for another.
-template <int DT, int D, int BLOCKS>
-__global__ __launch_bounds__(kJoinThreads) void tree_attention_join_kernel(
+// blocks of a tile).  A wave joins its share of the channels, kAhead parts' loads at
+// a time: over all parts where a tile has few, over every second group of them
+// where it has many (SPLIT = 2, one wave of each pair then adds the other's).  The
+// order of the sums is fixed.
+template <int DT, int D, int BLOCKS, int SPLIT>
+__global__ __launch_bounds__(kJoinThreads * SPLIT) void tree_attention_join_kernel(
     const TreeAttnArgs a, const AttnCut* __restrict__ cuts, const float* __restrict__ part_ml,
     const float* __restrict__ part_o) {
   constexpr int kDT = D / 16;
   constexpr int kMine = (kDT + kJoinWaves - 1) / kJoinWaves;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 4 * SPLIT;
   using E = El<DT>;
-  const int b = blockIdx.x;
+  __shared__ f32x4 sh_o[SPLIT > 1 ? kJoinWaves : 1][kMine][64];
+  __shared__ float sh_ml[SPLIT > 1 ? kJoinWaves : 1][2][64];
+  // In the order of the first launch: runs that tiles of equal length start in are a
+  // multiple of eight apart, and in the grid's own order one XCD would join them all
+  // (8 tiles of 33 parts: 57 us, so 15).
+  const int b = run_of(blockIdx.x, gridDim.x);
   const int blk = blockIdx.y;
   const AttnCut cut = cuts[b];
   const int row0 = cut.row0 + blk * 16;
   if (cut.parts == 0 || row0 >= cut.rows) return;
   const int lane = threadIdx.x & 63;
-  const int dt0 = uni(threadIdx.x >> 6) * kMine;
-  if (dt0 >= kDT) return;
+  const int wave = uni((threadIdx.x >> 6) & (kJoinWaves - 1));
+  const int share = uni(threadIdx.x >> 6) / kJoinWaves;   // of the parts
+  const int dt0 = wave * kMine;          // (past the last channel there is no output)
   float m = -INFINITY, l = 0.0f;
   f32x4 o[kMine];
 #pragma unroll
   for (int d = 0; d < kMine; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p0 = 0; p0 < cut.parts; p0 += kAhead) {
+  for (int p0 = share * kAhead; p0 < cut.parts; p0 += SPLIT * kAhead) {
     float m2[kAhead], l2[kAhead];
     f32x4 x[kAhead][kMine];
 #pragma unroll
@@ -1015,6 +1031,24 @@ __global__ __launch_bounds__(kJoinThreads) void tree_attention_join_kernel(
 #pragma unroll
       for (int d = 0; d < kMine; ++d) o[d] = o[d] * f1 + x[u][d] * f2;
     }
+  }
+  if constexpr (SPLIT > 1) {
+    if (share == 1) {
+      sh_ml[wave][0][lane] = m;
+      sh_ml[wave][1][lane] = l;
+#pragma unroll
+      for (int d = 0; d < kMine; ++d) sh_o[wave][d][lane] = o[d];
+    }
+    __syncthreads();
+    if (share == 1) return;
+    const float m2 = sh_ml[wave][0][lane];
+    const float nm = fmaxf(m, m2);
+    const float base = nm == -INFINITY ? 0.0f : nm;
+    const float f1 = pow2(m - base), f2 = pow2(m2 - base);
+    m = nm;
+    l = l * f1 + sh_ml[wave][1][lane] * f2;
+#pragma unroll
+    for (int d = 0; d < kMine; ++d) o[d] = o[d] * f1 + sh_o[wave][d][lane] * f2;
   }
   const int col = lane & 15, g = lane >> 4;
   const int row = row0 + col;
@@ -1050,9 +1084,10 @@ dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
                      p.whole, cuts, ml, po);
   const dspark_status st = check_launch("tree_attention_kernel");
   if (st != DSPARK_OK || p.whole) return st;
-  hipLaunchKernelGGL((tree_attention_join_kernel<DT, D, attn_group(D, RING) * NT>),
-                     dim3((unsigned)p.groups, (unsigned)p.row_blocks), dim3(kJoinThreads), 0, stream, a,
-                     cuts, ml, po);
+  auto join = p.deep ? &tree_attention_join_kernel<DT, D, attn_group(D, RING) * NT, 2>
+                     : &tree_attention_join_kernel<DT, D, attn_group(D, RING) * NT, 1>;
+  hipLaunchKernelGGL(join, dim3((unsigned)p.groups, (unsigned)p.row_blocks),
+                     dim3(kJoinThreads * (p.deep ? 2 : 1)), 0, stream, a, cuts, ml, po);
   return check_launch("tree_attention_join_kernel");
 }
 template <int DT, bool F8, int D>

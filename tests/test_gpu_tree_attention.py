@@ -157,6 +157,20 @@ def test_long_context_split_and_joined(tree):
 
 
 @pytest.mark.parametrize("Dh", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("n,ctx", [([1], [9000]), ([6], [1100]), ([50], [5000]), ([3, 64], [4000, 20])])
+def test_few_tiles_in_many_parts(n, ctx, Dh):
+    # one or two requests over all workgroups: tiles of up to dozens of parts
+    print(f"case attention many parts n={n} ctx={ctx} D={Dh}", flush=True)
+    c = make(320 + Dh, n, ctx, 4, 1, Dh, 16, "bf16", "e4m3" if Dh == 96 else "bf16", tree=len(n) == 1)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+    again, _ = call(c)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("Dh", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("P", [16, 32, 64, 256])
 @pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
 def test_many_rows_over_a_cut_context(Dh, P, dtype, cache):
