@@ -54,6 +54,7 @@
 //     product at 1170), between the matrix cores and the exponentials; the rest is
 //     each tile's start and end, and the parts (64 MB out and in, 18 us to join).
 //   One token over 200 positions: 7.2 us, the latency of dependent loads.
+//   6 tokens over 8000 positions: 28 us, over 130 thousand 111 us (4.8 TB/s).
 #pragma once
 
 #include <math.h>
