@@ -86,9 +86,11 @@ DSPARK_HD int64_t v_offset(int64_t page, int h, int d, int o, int Hk, int D, int
   return (((page * Hk + h) * D + d) << shift) + o;
 }
 
-// Whether an accepted path can be moved: path[0] = 0, then strictly increasing.
+// Whether an accepted path can be moved: path[0] = 0, then strictly increasing, so that
+// path[i] >= i.  That is asked for too: entries are judged apart, and one behind a bad
+// entry must not lead to a position before the segment.
 DSPARK_HD bool path_step_ok(const int32_t* path, int i) {
-  return i == 0 ? path[0] == 0 : path[i] > path[i - 1];
+  return i == 0 ? path[0] == 0 : path[i] > path[i - 1] && path[i] >= i;
 }
 
 // A parent link of node i.

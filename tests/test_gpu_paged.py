@@ -465,3 +465,21 @@ def test_lengths_beyond_an_int32_are_refused():
     path = dev(np.array([[0, 2, 3, -1], [0, 1, -1, -1]], np.int32))
     new = D.dspark_kv_commit(kc, vc, table, cur, path, dev(np.array([2, 1], np.int32)))
     assert new.tolist() == [-1, 7]
+
+
+@pytest.mark.parametrize("path", [[0, -5, -3, 4], [0, -2 ** 30, -2 ** 30 + 1, -2 ** 30 + 2], [0, -2 ** 31, -1, 3],
+                                  [-1, 0, 1, 2], [0, 2, 2, 3], [0, 1, 3, 2 ** 31 - 1]])
+def test_kv_commit_refuses_paths_out_of_the_segment(path):
+    # entries before the segment or past the table: nothing is moved, the other request is served
+    print(f"case kv_commit path {path}", flush=True)
+    rng = np.random.default_rng(6)
+    k, v = H.caches(rng, 8, 2, 64, 16, "bf16", DEV)
+    table = np.array([[3, 1, 6], [0, 7, 2]], np.int32)
+    ctx, acc = np.array([20, 21], np.int32), np.array([3, 3], np.int32)
+    both = np.array([path, [0, 2, 5, 9]], np.int64).astype(np.int32)
+    want = O.kv_commit(_raw(k)[None], _raw(v)[None], table, ctx, both, acc, 16)
+    assert want[2].tolist() == [-1, 25]
+    new = D.dspark_kv_commit(k, v, dev(table), dev(ctx), dev(both), dev(acc))
+    torch.cuda.synchronize()
+    assert np.array_equal(new.cpu().numpy(), want[2])
+    assert np.array_equal(_raw(k), want[0][0]) and np.array_equal(_raw(v), want[1][0])

@@ -141,6 +141,23 @@ def test_links_and_paths(shim):
         assert [shim.t_path(a, i) for i in range(3)] == good
 
 
+def test_every_entry_of_a_path_is_safe_by_itself(shim):
+    # Each entry is judged by a thread of its own, whatever the others find: one that passes is
+    # a node of the segment, at or behind its own place.
+    low = -2 ** 30
+    for path, good in (([0, -5, -3], [1, 0, 0]), ([0, low, low + 1], [1, 0, 0]), ([0, -BIG - 1, -BIG], [1, 0, 0]),
+                       ([0, 0, 1], [1, 0, 0]), ([0, 1, 2], [1, 1, 1]), ([0, 7, BIG], [1, 1, 1])):
+        a = (ctypes.c_int * 3)(*path)
+        assert [shim.t_path(a, i) for i in range(3)] == good, path
+    rng = np.random.default_rng(0)
+    for _ in range(300):
+        path = rng.integers(-4, 7, 5)
+        a = (ctypes.c_int * 5)(*path.tolist())
+        for i in range(5):
+            if shim.t_path(a, i):
+                assert path[i] >= i and (i == 0 or path[i] > path[i - 1])
+
+
 # ---- refusals of the C entry points ----
 
 @no_gpu
