@@ -165,6 +165,8 @@ def lib() -> ctypes.CDLL:
                                   vp, vp, vp, vp, vp]
     L.dspark_kv_commit.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, i32, i32, i32,
                                    i32, i32, i32, i32, vp, vp]
+    L.dspark_kv_commit_ex.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32,
+                                      i32, i32, i32, i32, i32, vp, vp]
     L.dspark_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32]
     L.dspark_tree_attention_workspace.restype = sz
     L.dspark_tree_attention.argtypes = [vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32,
@@ -173,6 +175,7 @@ def lib() -> ctypes.CDLL:
     L.dspark_tree_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     L.dspark_verify_tree.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
     for f in (L.dspark_page_map, L.dspark_page_trim, L.dspark_kv_store, L.dspark_kv_commit,
+              L.dspark_kv_commit_ex,
               L.dspark_tree_attention, L.dspark_tree_pack, L.dspark_verify_tree):
         f.restype = i32
     _LIB = L

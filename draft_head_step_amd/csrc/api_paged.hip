@@ -121,6 +121,18 @@ dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_str
                                const int32_t* path, const int32_t* accepted, int R, int max_nodes,
                                int Hk, int D, int page_size, int max_pages, int num_pages,
                                int32_t* new_len, void* stream) {
+  return dspark_kv_commit_ex(k_cache, v_cache, k_layer_stride, v_layer_stride, layers, cache_dtype,
+                             block_table, ctx_len, nullptr, path, accepted, R, max_nodes, Hk, D,
+                             page_size, max_pages, num_pages, new_len, stream);
+}
+
+dspark_status dspark_kv_commit_ex(void* k_cache, void* v_cache, int64_t k_layer_stride,
+                                  int64_t v_layer_stride, int layers, int cache_dtype,
+                                  const int32_t* block_table, const int32_t* ctx_len,
+                                  const int32_t* mapped_len, const int32_t* path,
+                                  const int32_t* accepted, int R, int max_nodes, int Hk, int D,
+                                  int page_size, int max_pages, int num_pages, int32_t* new_len,
+                                  void* stream) {
   dspark::clear_error();
   if (!k_cache || !v_cache || !block_table || !ctx_len || !path || !accepted || !new_len)
     return fail(DSPARK_EINVAL, "kv_commit: NULL required pointer");
@@ -140,12 +152,13 @@ dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_str
   // every layer's workgroups read the lengths, one of them writes the new ones
   const size_t lens = (size_t)R * sizeof(int32_t);
   if (dspark::overlap(new_len, lens, ctx_len, lens) ||
-      dspark::overlap(new_len, lens, accepted, lens))
+      dspark::overlap(new_len, lens, accepted, lens) ||
+      (mapped_len && dspark::overlap(new_len, lens, mapped_len, lens)))
     return fail(DSPARK_EINVAL, "kv_commit: new_len needs memory of its own");
   return dspark::launch_kv_commit(k_cache, v_cache, k_layer_stride, v_layer_stride, layers, el,
-                                  block_table, ctx_len, path, accepted, R, max_nodes, Hk, D,
-                                  dspark::page_shift(page_size), max_pages, num_pages, new_len,
-                                  reinterpret_cast<hipStream_t>(stream));
+                                  block_table, ctx_len, mapped_len, path, accepted, R, max_nodes,
+                                  Hk, D, dspark::page_shift(page_size), max_pages, num_pages,
+                                  new_len, reinterpret_cast<hipStream_t>(stream));
 }
 
 size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, int D) {

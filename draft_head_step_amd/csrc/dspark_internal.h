@@ -150,9 +150,10 @@ dspark_status launch_kv_store(const void* k, const void* v, int64_t k_stride, in
 dspark_status launch_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
                                int64_t v_layer_stride, int layers, int bytes_per_element,
                                const int32_t* block_table, const int32_t* ctx_len,
-                               const int32_t* path, const int32_t* accepted, int R, int max_nodes,
-                               int Hk, int D, int shift, int max_pages, int num_pages,
-                               int32_t* new_len, hipStream_t stream);
+                               const int32_t* mapped_len, const int32_t* path,
+                               const int32_t* accepted, int R, int max_nodes, int Hk, int D,
+                               int shift, int max_pages, int num_pages, int32_t* new_len,
+                               hipStream_t stream);
 // Arguments of the tree attention's kernels.
 struct TreeAttnArgs {
   const void* q;

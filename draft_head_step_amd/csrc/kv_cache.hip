@@ -173,8 +173,9 @@ template <int EL>
 __global__ __launch_bounds__(kT) void kv_commit_kernel(
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int64_t k_layer, int64_t v_layer,
     const int32_t* __restrict__ table, const int32_t* __restrict__ ctx_len,
-    const int32_t* __restrict__ path, const int32_t* __restrict__ accepted, int max_nodes, int Hk,
-    int D, int shift, int max_pages, int num_pages, int32_t* __restrict__ new_len) {
+    const int32_t* __restrict__ mapped_len, const int32_t* __restrict__ path,
+    const int32_t* __restrict__ accepted, int max_nodes, int Hk, int D, int shift, int max_pages,
+    int num_pages, int32_t* __restrict__ new_len) {
   constexpr int kC = 16 / EL;
   typedef std::conditional_t<EL == 1, uint8_t, uint16_t> V;
   __shared__ int bad, moves;
@@ -186,7 +187,9 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
   const int32_t* pages = table + (size_t)r * max_pages;
   const int64_t ctx = ctx_len[r];
   const int acc = accepted[r];
-  const int64_t room = min((int64_t)max_pages << shift, kMaxLen);
+  // what lies behind the mapped length is not the request's, whatever its row names there
+  const int64_t room = min(min((int64_t)max_pages << shift, kMaxLen),
+                           mapped_len ? (int64_t)mapped_len[r] : kMaxLen);
   if (t == 0) bad = moves = 0;
   __syncthreads();
   const bool range = ctx >= 0 && acc >= -1 && acc < max_nodes && ctx + 1 + acc <= room;
@@ -204,7 +207,8 @@ __global__ __launch_bounds__(kT) void kv_commit_kernel(
   }
   __syncthreads();
   const bool skip = bad != 0;
-  if (blockIdx.y == 0 && t == 0) new_len[r] = skip ? -1 : (int32_t)(ctx + 1 + acc);
+  if (blockIdx.y == 0 && t == 0)
+    new_len[r] = !skip ? (int32_t)(ctx + 1 + acc) : mapped_len ? (int32_t)ctx : -1;
   if (skip || !moves) return;   // a chain's path is where it belongs
   uint8_t* kc = k_cache + (int64_t)blockIdx.y * k_layer * EL;
   V* vc = reinterpret_cast<V*>(v_cache + (int64_t)blockIdx.y * v_layer * EL);
@@ -312,15 +316,16 @@ dspark_status launch_kv_store(const void* k, const void* v, int64_t k_stride, in
 dspark_status launch_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
                                int64_t v_layer_stride, int layers, int bytes_per_element,
                                const int32_t* block_table, const int32_t* ctx_len,
-                               const int32_t* path, const int32_t* accepted, int R, int max_nodes,
-                               int Hk, int D, int shift, int max_pages, int num_pages,
-                               int32_t* new_len, hipStream_t stream) {
+                               const int32_t* mapped_len, const int32_t* path,
+                               const int32_t* accepted, int R, int max_nodes, int Hk, int D,
+                               int shift, int max_pages, int num_pages, int32_t* new_len,
+                               hipStream_t stream) {
   const dim3 grid((unsigned)R, (unsigned)layers);
   auto kernel = bytes_per_element == 1 ? &kv_commit_kernel<1> : &kv_commit_kernel<2>;
   hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, stream, static_cast<uint8_t*>(k_cache),
                      static_cast<uint8_t*>(v_cache), k_layer_stride, v_layer_stride, block_table,
-                     ctx_len, path, accepted, max_nodes, Hk, D, shift, max_pages, num_pages,
-                     new_len);
+                     ctx_len, mapped_len, path, accepted, max_nodes, Hk, D, shift, max_pages,
+                     num_pages, new_len);
   return check_launch("kv_commit_kernel");
 }
 

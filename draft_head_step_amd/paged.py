@@ -213,13 +213,16 @@ def dspark_kv_store(k, v, slots, k_cache, v_cache, *, count=None, k_scale=None, 
         _D._check(st, "dspark_kv_store")
 
 
-def dspark_kv_commit(k_cache, v_cache, block_table, ctx_len, path, accepted, *, new_len=None,
-                     stream=None):
+def dspark_kv_commit(k_cache, v_cache, block_table, ctx_len, path, accepted, *, mapped_len=None,
+                     new_len=None, stream=None):
     """The accepted paths' keys and values to the front, in place.
 
     The caches are [pages, ...] or [layers, pages, ...] (layers may be strided);
     path [R, max_nodes] and accepted [R] as dspark_verify_tree returns them.
-    Returns new_len [R] = ctx_len + 1 + accepted."""
+    ``mapped_len`` [R] is new_len of dspark_page_map, needed wherever that call can
+    turn a request down: no position from there on is touched.  Returns new_len [R]
+    = ctx_len + 1 + accepted; a request whose path is refused moves nothing and
+    gets ctx_len with mapped_len, -1 without."""
     dev = _gpu(k_cache, "k_cache")
     lead = v_cache.dim() - 4
     if lead not in (0, 1):
@@ -242,14 +245,17 @@ def dspark_kv_commit(k_cache, v_cache, block_table, ctx_len, path, accepted, *, 
     _arr(ctx_len, "ctx_len", _I32, (R,), dev)
     _arr(path, "path", _I32, (R, nodes), dev)
     _arr(accepted, "accepted", _I32, (R,), dev)
+    if mapped_len is not None:
+        _arr(mapped_len, "mapped_len", _I32, (R,), dev)
     with _Call(dev, stream) as s:
         if new_len is None:
             new_len = ctx_len.new_empty((R,), dtype=_I32)
         _arr(new_len, "new_len", _I32, (R,), dev)
-        st = (_D._LIB or _D.lib()).dspark_kv_commit(
+        st = (_D._LIB or _D.lib()).dspark_kv_commit_ex(
             k_cache.data_ptr(), v_cache.data_ptr(), kl, vl, layers, _CACHE[k_cache.dtype],
-            block_table.data_ptr(), ctx_len.data_ptr(), path.data_ptr(), accepted.data_ptr(), R,
-            nodes, hk, d, p, mp, n, new_len.data_ptr(), s)
+            block_table.data_ptr(), ctx_len.data_ptr(),
+            0 if mapped_len is None else mapped_len.data_ptr(), path.data_ptr(),
+            accepted.data_ptr(), R, nodes, hk, d, p, mp, n, new_len.data_ptr(), s)
     if st:
         _D._check(st, "dspark_kv_commit")
     return new_len

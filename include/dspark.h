@@ -584,9 +584,11 @@ dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, in
  * outside [-1, max_nodes), or that touches a page id outside [0, num_pages) or
  * a position past its table or 2^31 - 1 moves nothing and gets new_len[r] = -1.
  *   new_len     [R] int32 output, apart from ctx_len and accepted.
+ * Behind the pages that a request holds its block_table row may name pages of
+ * others: where a pool can run short, dspark_kv_commit_ex is the call to use.
  * Errors: EINVAL for NULL pointers, sizes <= 0, a bad page size or type,
- * misaligned caches or strides, new_len on ctx_len or accepted; EUNSUPPORTED for D as above, layers > 65535 or
- * R > 65535; EDEVICE.
+ * misaligned caches or strides, new_len on ctx_len or accepted; EUNSUPPORTED
+ * for D as above, layers > 65535 or R > 65535; EDEVICE.
  */
 dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
                                int64_t v_layer_stride, int layers, int cache_dtype,
@@ -594,6 +596,26 @@ dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_str
                                const int32_t* path, const int32_t* accepted, int R, int max_nodes,
                                int Hk, int D, int page_size, int max_pages, int num_pages,
                                int32_t* new_len, void* stream);
+
+/*
+ * dspark_kv_commit for requests whose elements dspark_page_map may have turned
+ * down.
+ *   mapped_len  [R] int32 (dspark_page_map's new_len) or NULL, which is
+ *               dspark_kv_commit: no position from mapped_len[r] on is read or
+ *               written.
+ * With mapped_len a request that dspark_kv_commit would refuse, or whose path
+ * leads to mapped_len[r] or behind it, moves nothing and keeps its context:
+ * new_len[r] = ctx_len[r].  dspark_page_trim from mapped_len to new_len then
+ * gives back the pages of what was not accepted, and no others.
+ * Errors: as dspark_kv_commit, plus EINVAL for new_len on mapped_len.
+ */
+dspark_status dspark_kv_commit_ex(void* k_cache, void* v_cache, int64_t k_layer_stride,
+                                  int64_t v_layer_stride, int layers, int cache_dtype,
+                                  const int32_t* block_table, const int32_t* ctx_len,
+                                  const int32_t* mapped_len, const int32_t* path,
+                                  const int32_t* accepted, int R, int max_nodes, int Hk, int D,
+                                  int page_size, int max_pages, int num_pages, int32_t* new_len,
+                                  void* stream);
 
 /* Bytes of workspace dspark_tree_attention needs (0 if invalid).  It depends on
  * the current device's number of compute units. */

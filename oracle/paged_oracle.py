@@ -87,18 +87,19 @@ def kv_store(k, v, slots, k_cache, v_cache, P, count=None):
     return k_cache, v_cache
 
 
-def kv_commit(k_cache, v_cache, table, ctx, path, accepted, P):
+def kv_commit(k_cache, v_cache, table, ctx, path, accepted, P, mapped=None):
     """[layers, pages, ...] caches.  Returns copies after the move, and new_len."""
     k_cache, v_cache = k_cache.copy(), v_cache.copy()
     R, width = table.shape
     n_pages = k_cache.shape[1]
-    new_len = np.full(R, -1, np.int32)
+    new_len = np.full(R, -1, np.int32) if mapped is None else np.array(ctx, np.int32)
     for r in range(R):
         c, a = int(ctx[r]), int(accepted[r])
-        if c < 0 or a < -1 or a >= path.shape[1] or c + 1 + a > width * P:
+        room = width * P if mapped is None else min(width * P, int(mapped[r]))
+        if c < 0 or a < -1 or a >= path.shape[1] or c + 1 + a > room:
             continue
         p = [int(x) for x in path[r, :a + 1]]
-        if a >= 0 and (p[0] != 0 or any(y <= x for x, y in zip(p, p[1:])) or c + p[-1] >= width * P):
+        if a >= 0 and (p[0] != 0 or any(y <= x for x, y in zip(p, p[1:])) or c + p[-1] >= room):
             continue
         moves = [(c + p[i], c + i) for i in range(1, a + 1)]
         if any(not 0 <= table[r, t // P] < n_pages for m in moves for t in m):

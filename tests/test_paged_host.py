@@ -274,6 +274,21 @@ def test_verify_tree_rejects(kw, want):
                                       a["acc"], a["path"], a["nxt"], None) == want
 
 
+@no_gpu
+@pytest.mark.parametrize("kw,want", [
+    (dict(kc=None), EINVAL), (dict(acc=None), EINVAL), (dict(R=0), EINVAL), (dict(D=72), EUNSUPPORTED), (dict(ps=20), EINVAL),
+    (dict(mapped=4 * P, new=4 * P), EINVAL), (dict(mapped=4 * P, new=4 * P - 4), EINVAL), (dict(new=P), EINVAL),
+])
+def test_kv_commit_ex_rejects(kw, want):
+    a = dict(kc=P, vc=P, kl=0, vl=0, L=1, ct=0, table=P, ctx=P, mapped=2 * P, path=P, acc=P, R=2, nodes=8, Hk=2, D=64, ps=16,
+             mp=4, np_=9, new=3 * P)
+    a.update(kw)
+    assert D.lib().dspark_kv_commit_ex(a["kc"], a["vc"], a["kl"], a["vl"], a["L"], a["ct"], a["table"], a["ctx"], a["mapped"],
+                                       a["path"], a["acc"], a["R"], a["nodes"], a["Hk"], a["D"], a["ps"], a["mp"], a["np_"],
+                                       a["new"], None) == want
+    assert D.lib().dspark_last_error() != b""
+
+
 # ---- refusals of the binding: nothing that is not on a device is taken ----
 
 def test_binding_refuses_host_tensors():
@@ -337,3 +352,19 @@ def test_oracle_trees_by_hand():
     assert acc.tolist() == [1] and path.tolist() == [[0, 1, -1, -1]] and nxt.tolist() == [7]
     acc, path, nxt, top = O.verify_tree(logits, np.array([0, 6]), np.array([0, 4, 4, 1, 7, 7]), par, 6)
     assert acc.tolist() == [2] and path[0, :3].tolist() == [0, 1, 5] and nxt.tolist() == [2]
+
+
+def test_oracle_of_a_short_pool():
+    # 15 and 14 tokens, one free page that both rows still name: the second request is turned
+    # down, and its path must not move into the page that the first was given
+    table = np.array([[0, 2, -1], [1, 2, -1]], np.int32)
+    cur, cu = np.array([15, 14]), np.array([0, 3, 8])
+    t, s, new, pool = O.page_map(cur, cu, table, np.array([2, -1, -1]), np.array([0, 1, 0, 0]), 16, 8, np.full(8, -9))
+    assert new.tolist() == [18, 14] and pool.tolist() == [1, 0, 1, 0] and s.tolist() == [15, 32, 33, -1, -1, -1, -1, -1]
+    k, v = np.arange(3 * 16.0).reshape(1, 3, 1, 1, 16, 1), np.arange(3 * 16.0).reshape(1, 3, 1, 1, 16)
+    path, acc = np.array([[0, 2, -1], [0, 2, 4]]), np.array([1, 2])
+    _, v2, kept = O.kv_commit(k, v, t, cur, path, acc, 16)
+    assert kept.tolist() == [17, 17] and v2[0, 2, 0, 0, 0] != v[0, 2, 0, 0, 1]
+    _, v2, kept = O.kv_commit(k, v, t, cur, path, acc, 16, new)
+    assert kept.tolist() == [17, 14] and v2[0, 2, 0, 0, 0] == v[0, 2, 0, 0, 1]
+    assert (v2 != v).sum() == 1
