@@ -177,6 +177,23 @@ dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
                                     int page_size, int max_pages, int num_pages, float scale,
                                     void* out, int64_t out_stride, float* lse, void* workspace,
                                     size_t ws_bytes, void* stream) {
+  return dspark_tree_attention_ex(q, q_stride, dtype, k_cache, v_cache, cache_dtype, k_scale,
+                                  v_scale, block_table, ctx_len, nullptr, cu_seqlens, tree_mask,
+                                  mask_words, R, max_tokens, Hq, Hk, D, page_size, max_pages,
+                                  num_pages, scale, out, out_stride, lse, workspace, ws_bytes,
+                                  stream);
+}
+
+dspark_status dspark_tree_attention_ex(const void* q, int64_t q_stride, int dtype,
+                                       const void* k_cache, const void* v_cache, int cache_dtype,
+                                       const float* k_scale, const float* v_scale,
+                                       const int32_t* block_table, const int32_t* ctx_len,
+                                       const int32_t* mapped_len, const int32_t* cu_seqlens,
+                                       const uint32_t* tree_mask, int mask_words, int R,
+                                       int max_tokens, int Hq, int Hk, int D, int page_size,
+                                       int max_pages, int num_pages, float scale, void* out,
+                                       int64_t out_stride, float* lse, void* workspace,
+                                       size_t ws_bytes, void* stream) {
   dspark::clear_error();
   if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !cu_seqlens || !out)
     return fail(DSPARK_EINVAL, "tree_attention: NULL required pointer");
@@ -217,6 +234,7 @@ dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
   a.v_scale = v_scale;
   a.table = block_table;
   a.ctx = ctx_len;
+  a.mapped = mapped_len;
   a.cu = cu_seqlens;
   a.mask = tree_mask;
   a.out = out;

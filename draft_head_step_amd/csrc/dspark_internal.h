@@ -163,6 +163,7 @@ struct TreeAttnArgs {
   const float* v_scale;
   const int32_t* table;
   const int32_t* ctx;
+  const int32_t* mapped;   // positions that a request holds, or NULL
   const int32_t* cu;
   const uint32_t* mask;
   void* out;

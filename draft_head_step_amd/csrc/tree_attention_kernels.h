@@ -265,6 +265,7 @@ __device__ __forceinline__ Req request(const TreeAttnArgs& a, int r, int group, 
   q.n = (int)n;
   q.rows = here > 0 ? (int)here * group : 0;
   q.bad = ctx < 0 || total > 0x7fff0000LL || pages_of(total < 0 ? 0 : total, a.shift) > a.max_pages;
+  if (a.mapped) q.bad |= total > a.mapped[r];   // what its row names there is not its own
   q.ctx = q.bad ? 0 : (int)ctx;
   q.total = q.bad ? 0 : (int)total;
   constexpr int kTile = 16 * NT * WAVES;

@@ -266,13 +266,14 @@ def dspark_tree_attention_workspace(R: int, max_tokens: int, Hq: int, Hk: int, D
 
 
 def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens, scale=None, *,
-                          tree_mask=None, k_scale=None, v_scale=None, out=None, lse=None,
-                          want_lse=False, workspace=None, stream=None):
+                          tree_mask=None, mapped_len=None, k_scale=None, v_scale=None, out=None,
+                          lse=None, want_lse=False, workspace=None, stream=None):
     """Attention of q [N, Hq, D] (bfloat16 or float16, dense heads, any row stride) over
     each request's cached context and its own segment: causal, or by tree_mask
-    [N, words] int32 / uint32.  ``scale`` is 1 / sqrt(D) by default.  Returns
-    (out [N, Hq, D], lse [N, Hq] fp32 or None); rows beyond cu_seqlens[R] are not
-    written."""
+    [N, words] int32 / uint32.  ``scale`` is 1 / sqrt(D) by default.  ``mapped_len``
+    [R] is new_len of dspark_page_map: rows of a request that it turned down are NaN.
+    Returns (out [N, Hq, D], lse [N, Hq] fp32 or None); rows beyond cu_seqlens[R] are
+    not written."""
     dev = _gpu(q, "q")
     n, hk, d, p = _cache_shape(k_cache, v_cache)
     _dense(k_cache, "k_cache")
@@ -287,6 +288,8 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens,
     _arr(block_table, "block_table", _I32, (R, mp), dev)
     _arr(ctx_len, "ctx_len", _I32, (R,), dev)
     _arr(cu_seqlens, "cu_seqlens", _I32, (R + 1,), dev)
+    if mapped_len is not None:
+        _arr(mapped_len, "mapped_len", _I32, (R,), dev)
     words = 0
     if tree_mask is not None:
         words = tree_mask.shape[-1]
@@ -309,11 +312,11 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens,
             workspace = q.new_empty((max(need, 1),), dtype=torch.uint8)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
-        st = L.dspark_tree_attention(
+        st = L.dspark_tree_attention_ex(
             q.data_ptr(), qs, _CACHE[q.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
             _CACHE[k_cache.dtype], sk, sv, block_table.data_ptr(), ctx_len.data_ptr(),
-            cu_seqlens.data_ptr(), 0 if tree_mask is None else tree_mask.data_ptr(), words, R, N,
-            hq, hk, d, p, mp, n, 1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
+            0 if mapped_len is None else mapped_len.data_ptr(), cu_seqlens.data_ptr(),
+            0 if tree_mask is None else tree_mask.data_ptr(), words, R, N, hq, hk, d, p, mp, n, 1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
             os_, 0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), s)
     if st:

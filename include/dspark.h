@@ -672,6 +672,27 @@ dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
                                     size_t ws_bytes, void* stream);
 
 /*
+ * dspark_tree_attention for requests whose elements dspark_page_map may have
+ * turned down.
+ *   mapped_len  [R] int32 (dspark_page_map's new_len) or NULL, which is
+ *               dspark_tree_attention.  A request with more positions than
+ *               mapped_len[r] (ctx_len[r] and its elements) does not hold them,
+ *               whatever its block_table row names behind its last page: its
+ *               rows are NaN and no page of it is read.
+ * Errors: as dspark_tree_attention.
+ */
+dspark_status dspark_tree_attention_ex(const void* q, int64_t q_stride, int dtype,
+                                       const void* k_cache, const void* v_cache, int cache_dtype,
+                                       const float* k_scale, const float* v_scale,
+                                       const int32_t* block_table, const int32_t* ctx_len,
+                                       const int32_t* mapped_len, const int32_t* cu_seqlens,
+                                       const uint32_t* tree_mask, int mask_words, int R,
+                                       int max_tokens, int Hq, int Hk, int D, int page_size,
+                                       int max_pages, int num_pages, float scale, void* out,
+                                       int64_t out_stride, float* lse, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/*
  * A forest of drafted nodes in the form that the attention reads.  parents[e]
  * is the segment-local number of element e's parent, smaller than its own, or
  * -1 for a root.

@@ -167,7 +167,8 @@ def verify_tree(logits, cu, tokens, parents, max_nodes):
     return accepted, path, nxt, top
 
 
-def tree_attention(q, k_cache, v_cache, table, ctx, cu, P, scale, mask=None, k_scale=None, v_scale=None):
+def tree_attention(q, k_cache, v_cache, table, ctx, cu, P, scale, mask=None, k_scale=None, v_scale=None,
+                   mapped=None):
     """Returns (out [N, Hq, D], lse [N, Hq], weight [N, Hq, D], size [N, Hq], top [N, Hq]) in
     64 bits: weight = sum_t p_t |v_t|, size = the largest scale * sum_d |q_d k_td| that a
     row sees and top the largest |score|, for error bounds.  Rows of a request whose
@@ -184,7 +185,8 @@ def tree_attention(q, k_cache, v_cache, table, ctx, cu, P, scale, mask=None, k_s
             continue
         total = cx + n
         need = _up(total, P) if cx >= 0 else 0
-        if cx < 0 or need > width or any(not 0 <= p < n_pages for p in table[r, :need]):
+        held = mapped is None or total <= mapped[r]
+        if cx < 0 or not held or need > width or any(not 0 <= p < n_pages for p in table[r, :need]):
             out[lo:lo + n], lse[lo:lo + n] = np.nan, np.nan
             continue
         pages = table[r, :need]

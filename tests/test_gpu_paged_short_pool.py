@@ -26,6 +26,15 @@ def _raw(t):
     return t.view(torch.uint8 if t.element_size() == 1 else torch.int16).cpu().numpy()
 
 
+def attention_bound(ref, T):
+    """Error bound of bf16 rows against the oracle's (out, lse, W, A, M): the result's own
+    rounding u, the probabilities' u on W, and e and (T + 16) f of the fp32 scores and sums."""
+    u, f = H.half_step(torch.bfloat16), 2.0 ** -24
+    out, _, W, A, M = ref
+    e = 2 * ((out.shape[2] + 4) * f * A + 4 * f * (2 * M + 2))[..., None]
+    return u * np.abs(out) * (1 + e) + W * (u + e + 2 * (T + 16) * f) + 2.0 ** -126
+
+
 # Two requests of 15 and 14 tokens with one free page, 2, which both rows name behind the
 # page that their request holds: the first is given it, the second is turned down.
 P = 16
@@ -97,3 +106,56 @@ def test_commit_with_mapped_lengths_keeps_the_context_of_refused_paths():
     with pytest.raises(D.DsparkError):
         m = dev(mapped_len)
         D.dspark_kv_commit(k, v, dev(table), dev(cur), dev(path), dev(acc), mapped_len=m, new_len=m)
+
+
+@pytest.mark.parametrize("ring", [False, True])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_reads_no_pages_of_others(tree, ring):
+    # the rows of the request that was turned down are NaN, the others' are computed
+    print(f"case short pool attention tree={tree} ring={ring}", flush=True)
+    rng = np.random.default_rng(3)
+    g = 16 if ring else 1
+    k, v = H.caches(rng, 3, 2, 64, P, "bf16", DEV)
+    table, cu, _, new = mapped()
+    q = torch.from_numpy(rng.normal(0, 1, (8, 2 * g, 64)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    mask = dev(np.array([[1], [3], [5], [1], [3], [7], [9], [17]], np.int32)) if tree else None
+    out, lse = D.dspark_tree_attention(q, k, v, table, dev(CUR), cu, tree_mask=mask, mapped_len=new, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[3:]).all() and torch.isnan(lse[3:]).all()
+    ref = O.tree_attention(H.np64(q), H.np64(k), H.np64(v), table.cpu().numpy(), CUR, H.starts(N), P, 0.125,
+                           None if mask is None else mask.cpu().numpy().view(np.uint32), mapped=new.cpu().numpy())
+    assert np.isnan(ref[0][3:]).all() and np.isfinite(ref[0][:3]).all()
+    assert (np.abs(H.np64(out) - ref[0]) <= attention_bound(ref, 18))[:3].all()
+    # a length that the elements fill exactly is held
+    full = dev((CUR + np.array(N)).astype(np.int32))
+    a = D.dspark_tree_attention(q, k, v, table, dev(CUR), cu, tree_mask=mask, mapped_len=full)[0]
+    b = D.dspark_tree_attention(q, k, v, table, dev(CUR), cu, tree_mask=mask)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.isfinite(a).all()
+    with pytest.raises(ValueError):
+        D.dspark_tree_attention(q, k, v, table, dev(CUR), cu, mapped_len=full[:1])
+    with pytest.raises(TypeError):
+        D.dspark_tree_attention(q, k, v, table, dev(CUR), cu, mapped_len=full.float())
+
+
+def test_attention_of_many_requests_with_some_turned_down():
+    # cut tiles, several requests a workgroup, refused ones between served ones
+    print("case short pool attention many", flush=True)
+    rng = np.random.default_rng(4)
+    R = 30
+    cur = rng.integers(0, 900, R).astype(np.int32)
+    n = rng.integers(0, 9, R)
+    cu = H.starts(n)
+    pages = int(sum(-(-int(x) // P) for x in cur + n)) + 2
+    k, v = H.caches(rng, pages, 2, 128, P, "bf16", DEV)
+    table = H.tables(rng, cur + n, P, pages)
+    held = np.where(rng.random(R) < 0.4, cur, cur + n).astype(np.int32)
+    q = torch.from_numpy(rng.normal(0, 1, (int(cu[-1]), 8, 128)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    a, la = D.dspark_tree_attention(q, k, v, dev(table), dev(cur), dev(cu), mapped_len=dev(held), want_lse=True)
+    ref = O.tree_attention(H.np64(q), H.np64(k), H.np64(v), table, cur, cu, P, 128 ** -0.5, mapped=held)
+    torch.cuda.synchronize()
+    down = np.isnan(ref[0][:, 0, 0])   # their weights are zeros
+    assert 5 < down.sum() < len(down) - 5
+    got = H.np64(a)
+    assert np.isnan(got[down]).all() and np.isnan(la.cpu().numpy()[down]).all()
+    assert (np.abs(got - ref[0]) <= attention_bound(ref, 910))[~down].all()

@@ -289,6 +289,20 @@ def test_kv_commit_ex_rejects(kw, want):
     assert D.lib().dspark_last_error() != b""
 
 
+@no_gpu
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(R=0), EINVAL), (dict(Hq=9), EINVAL), (dict(D=48, qs=512), EUNSUPPORTED),
+    (dict(scale=float("nan")), EINVAL), (dict(ws=None), EWORKSPACE),
+])
+def test_tree_attention_ex_rejects(kw, want):
+    a = dict(q=P, qs=512, out=2 * P, R=2, N=4, Hq=8, Hk=2, D=64, scale=0.125, ws=P)
+    a.update(kw)
+    assert D.lib().dspark_tree_attention_ex(a["q"], a["qs"], 0, P, P, 0, None, None, P, P, 3 * P, P, None, 0, a["R"], a["N"],
+                                            a["Hq"], a["Hk"], a["D"], 16, 4, 9, a["scale"], a["out"], 512, None, a["ws"],
+                                            1 << 40, None) == want
+    assert D.lib().dspark_last_error() != b""
+
+
 # ---- refusals of the binding: nothing that is not on a device is taken ----
 
 def test_binding_refuses_host_tensors():
