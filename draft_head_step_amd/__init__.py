@@ -177,9 +177,11 @@ def lib() -> ctypes.CDLL:
                                            i64, vp, vp, sz, vp]
     L.dspark_tree_pack.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     L.dspark_verify_tree.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.dspark_verify_tree_ex.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp,
+                                        vp]
     for f in (L.dspark_page_map, L.dspark_page_trim, L.dspark_kv_store, L.dspark_kv_commit,
               L.dspark_kv_commit_ex, L.dspark_tree_attention, L.dspark_tree_attention_ex,
-              L.dspark_tree_pack, L.dspark_verify_tree):
+              L.dspark_tree_pack, L.dspark_verify_tree, L.dspark_verify_tree_ex):
         f.restype = i32
     _LIB = L
     return L

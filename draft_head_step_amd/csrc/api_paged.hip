@@ -277,14 +277,28 @@ dspark_status dspark_verify_tree(const float* target_logits, const int32_t* cu_s
                                  int max_tokens, int max_nodes, int V, int32_t* target_argmax,
                                  int32_t* accepted, int32_t* path, int32_t* next_token,
                                  void* stream) {
+  return dspark_verify_tree_ex(target_logits, cu_seqlens, tokens, parents, nullptr, nullptr, R,
+                               max_tokens, max_nodes, V, target_argmax, accepted, path,
+                               next_token, stream);
+}
+
+dspark_status dspark_verify_tree_ex(const float* target_logits, const int32_t* cu_seqlens,
+                                    const int32_t* tokens, const int32_t* parents,
+                                    const int32_t* ctx_len, const int32_t* mapped_len, int R,
+                                    int max_tokens, int max_nodes, int V, int32_t* target_argmax,
+                                    int32_t* accepted, int32_t* path, int32_t* next_token,
+                                    void* stream) {
   dspark::clear_error();
   if (!target_logits || !cu_seqlens || !tokens || !parents || !target_argmax || !accepted ||
       !path || !next_token)
     return fail(DSPARK_EINVAL, "verify_tree: NULL required pointer");
   if (R <= 0 || max_tokens <= 0 || max_nodes <= 0 || V < 1)
     return fail(DSPARK_EINVAL, "verify_tree: sizes must be positive");
-  return dspark::launch_verify_tree(target_logits, cu_seqlens, tokens, parents, R, max_tokens,
-                                    max_nodes, V, target_argmax, accepted, path, next_token,
+  if (!ctx_len != !mapped_len)
+    return fail(DSPARK_EINVAL, "verify_tree: ctx_len and mapped_len go together");
+  return dspark::launch_verify_tree(target_logits, cu_seqlens, tokens, parents, ctx_len,
+                                    mapped_len, R, max_tokens, max_nodes, V, target_argmax,
+                                    accepted, path, next_token,
                                     reinterpret_cast<hipStream_t>(stream));
 }
 

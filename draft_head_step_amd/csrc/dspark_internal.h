@@ -180,7 +180,8 @@ dspark_status launch_tree_pack(const int32_t* parents, const int32_t* cu, const 
                                int R, int max_tokens, int mask_words, uint32_t* mask,
                                int32_t* flat_pos, int32_t* flat_req, hipStream_t stream);
 dspark_status launch_verify_tree(const float* logits, const int32_t* cu, const int32_t* tokens,
-                                 const int32_t* parents, int R, int max_tokens, int max_nodes,
+                                 const int32_t* parents, const int32_t* ctx_len,
+                                 const int32_t* mapped_len, int R, int max_tokens, int max_nodes,
                                  int V, int32_t* amax, int32_t* accepted, int32_t* path,
                                  int32_t* next_token, hipStream_t stream);
 

@@ -235,7 +235,8 @@ __global__ __launch_bounds__(kRowT) void verify_argmax_kernel(const float* __res
 // nodes, behind 99 us for the argmaxes of their 1188 rows of 129280 (6.2 TB/s).
 __global__ __launch_bounds__(64) void verify_walk_kernel(
     const int32_t* __restrict__ amax, const int32_t* __restrict__ cu,
-    const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents, int max_tokens,
+    const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents,
+    const int32_t* __restrict__ ctx_len, const int32_t* __restrict__ mapped_len, int max_tokens,
     int max_nodes, int32_t* __restrict__ accepted, int32_t* __restrict__ path,
     int32_t* __restrict__ next_token) {
   const int r = blockIdx.x;
@@ -243,6 +244,8 @@ __global__ __launch_bounds__(64) void verify_walk_kernel(
   const int32_t s = cu[r];
   const int64_t end = min((int64_t)cu[r + 1], (int64_t)max_tokens);
   int64_t len = s < 0 ? 0 : end - s;
+  // elements that the request got no places for are none
+  if (mapped_len && (int64_t)ctx_len[r] + cu[r + 1] - s > mapped_len[r]) len = 0;
   const int n = (int)(len < 0 ? 0 : len > max_nodes ? max_nodes : len);
   int32_t* row = path + (size_t)r * max_nodes;
   int count = 0;       // nodes on the path
@@ -616,13 +619,14 @@ dspark_status launch_row_argmax(const float* logits, const int32_t* n_rows, int 
 }
 
 dspark_status launch_verify_tree(const float* logits, const int32_t* cu, const int32_t* tokens,
-                                 const int32_t* parents, int R, int max_tokens, int max_nodes,
+                                 const int32_t* parents, const int32_t* ctx_len,
+                                 const int32_t* mapped_len, int R, int max_tokens, int max_nodes,
                                  int V, int32_t* amax, int32_t* accepted, int32_t* path,
                                  int32_t* next_token, hipStream_t stream) {
   const dspark_status st = launch_row_argmax(logits, cu + R, max_tokens, V, amax, stream);
   if (st != DSPARK_OK) return st;
   hipLaunchKernelGGL(verify_walk_kernel, dim3(R), dim3(64), 0, stream, amax, cu, tokens, parents,
-                     max_tokens, max_nodes, accepted, path, next_token);
+                     ctx_len, mapped_len, max_tokens, max_nodes, accepted, path, next_token);
   return check_launch("verify_walk_kernel");
 }
 

@@ -356,10 +356,13 @@ def dspark_tree_pack(parents, cu_seqlens, mask_words, pos0=None, *, mask=None, f
     return (mask, flat_pos, flat_req) if flat_req is not None else (mask, flat_pos)
 
 
-def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *,
-                       target_argmax=None, accepted=None, path=None, next_token=None, stream=None):
+def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *, ctx_len=None,
+                       mapped_len=None, target_argmax=None, accepted=None, path=None,
+                       next_token=None, stream=None):
     """Greedy verification of trees over a flattened batch: target_logits [N, V] fp32,
-    tokens and parents [N] int32, node 0 of each segment its anchor.  Returns
+    tokens and parents [N] int32, node 0 of each segment its anchor.  With ``ctx_len`` and
+    ``mapped_len`` [R] (cur_len and new_len of dspark_page_map) a request that it
+    turned down counts as an empty segment.  Returns
     (accepted [R], path [R, max_nodes], next_token [R], target_argmax [N])."""
     dev = _gpu(tokens, "tokens")
     N, = tokens.shape
@@ -371,6 +374,11 @@ def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *,
         raise ValueError("target_logits must be [N, V]")
     V = target_logits.shape[1]
     _arr(target_logits, "target_logits", _F32, (N, V), dev)
+    if (ctx_len is None) != (mapped_len is None):
+        raise ValueError("ctx_len and mapped_len go together")
+    if mapped_len is not None:
+        _arr(ctx_len, "ctx_len", _I32, (R,), dev)
+        _arr(mapped_len, "mapped_len", _I32, (R,), dev)
     with _Call(dev, stream) as s:
         if target_argmax is None:
             target_argmax = tokens.new_empty((N,), dtype=_I32)
@@ -384,9 +392,10 @@ def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *,
         _arr(accepted, "accepted", _I32, (R,), dev)
         _arr(path, "path", _I32, (R, max_nodes), dev)
         _arr(next_token, "next_token", _I32, (R,), dev)
-        st = (_D._LIB or _D.lib()).dspark_verify_tree(
+        st = (_D._LIB or _D.lib()).dspark_verify_tree_ex(
             target_logits.data_ptr(), cu_seqlens.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
-            R, N, max_nodes, V, target_argmax.data_ptr(), accepted.data_ptr(), path.data_ptr(),
+            0 if mapped_len is None else ctx_len.data_ptr(),
+            0 if mapped_len is None else mapped_len.data_ptr(), R, N, max_nodes, V, target_argmax.data_ptr(), accepted.data_ptr(), path.data_ptr(),
             next_token.data_ptr(), s)
     if st:
         _D._check(st, "dspark_verify_tree")

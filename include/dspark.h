@@ -469,6 +469,16 @@ dspark_status dspark_accept_prob(const float* draft_logits, const float* target_
  * OCP e4m3 (finite values up to 448) with one scale per head for the keys and
  * one for the values.
  *
+ * A pool that runs short.  dspark_page_map turns a request down on the device,
+ * and the calls behind it have already been enqueued.  They learn of it from
+ * mapped_len, its new_len (dspark_tree_attention_ex, dspark_verify_tree_ex,
+ * dspark_kv_commit_ex): the request's rows are NaN, nothing is accepted, no page
+ * is written, and it keeps its context for another step.  Without mapped_len they
+ * go by block_table, which names pages of others behind a request's last page.
+ * For chains, which need no commit, the length to keep is
+ * min(ctx_len + 1 + accepted, mapped_len); where that is ctx_len the request was
+ * turned down and its next token is not one.
+ *
  * Outputs share no memory with inputs or with each other unless an entry says
  * that they may.
  * ------------------------------------------------------------------------ */
@@ -731,6 +741,24 @@ dspark_status dspark_verify_tree(const float* target_logits, const int32_t* cu_s
                                  int max_tokens, int max_nodes, int V, int32_t* target_argmax,
                                  int32_t* accepted, int32_t* path, int32_t* next_token,
                                  void* stream);
+
+/*
+ * dspark_verify_tree for requests whose elements dspark_page_map may have turned
+ * down.
+ *   ctx_len, mapped_len  [R] int32 (cur_len and new_len of dspark_page_map), or
+ *               both NULL, which is dspark_verify_tree.  A request with more
+ *               positions than mapped_len[r] (ctx_len[r] and its elements) counts as
+ *               an empty segment: accepted -1, a path of -1, next_token -1.  Its rows'
+ *               argmaxes are written; its logits may be NaN.
+ * Errors: as dspark_verify_tree, plus EINVAL for one of the two without the
+ * other.
+ */
+dspark_status dspark_verify_tree_ex(const float* target_logits, const int32_t* cu_seqlens,
+                                    const int32_t* tokens, const int32_t* parents,
+                                    const int32_t* ctx_len, const int32_t* mapped_len, int R,
+                                    int max_tokens, int max_nodes, int V, int32_t* target_argmax,
+                                    int32_t* accepted, int32_t* path, int32_t* next_token,
+                                    void* stream);
 
 /* Static description of a status code. */
 const char* dspark_status_string(int status);

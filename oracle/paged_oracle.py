@@ -146,14 +146,14 @@ def tree_pack(parents, cu, pos0, words):
     return mask, pos, req
 
 
-def verify_tree(logits, cu, tokens, parents, max_nodes):
+def verify_tree(logits, cu, tokens, parents, max_nodes, ctx=None, mapped=None):
     top = np.argmax(logits, axis=1).astype(np.int32)
     R = len(cu) - 1
     path = np.full((R, max_nodes), -1, np.int32)
     accepted, nxt = np.full(R, -1, np.int32), np.full(R, -1, np.int32)
     for r in range(R):
         lo, n = int(cu[r]), min(int(cu[r + 1] - cu[r]), max_nodes)
-        if n <= 0:
+        if n <= 0 or (mapped is not None and int(ctx[r]) + int(cu[r + 1] - cu[r]) > mapped[r]):
             continue
         walk = [0]
         while True:

@@ -154,8 +154,117 @@ def test_attention_of_many_requests_with_some_turned_down():
     a, la = D.dspark_tree_attention(q, k, v, dev(table), dev(cur), dev(cu), mapped_len=dev(held), want_lse=True)
     ref = O.tree_attention(H.np64(q), H.np64(k), H.np64(v), table, cur, cu, P, 128 ** -0.5, mapped=held)
     torch.cuda.synchronize()
-    down = np.isnan(ref[0][:, 0, 0])   # their weights are zeros
+    down = np.isnan(ref[0][:, 0, 0])
     assert 5 < down.sum() < len(down) - 5
     got = H.np64(a)
     assert np.isnan(got[down]).all() and np.isnan(la.cpu().numpy()[down]).all()
     assert (np.abs(got - ref[0]) <= attention_bound(ref, 910))[~down].all()
+
+
+def test_acceptance_takes_nothing_of_a_request_that_was_turned_down():
+    print("case short pool acceptance", flush=True)
+    rng = np.random.default_rng(5)
+    R, V, nodes = 40, 97, 8
+    cur = rng.integers(0, 100, R).astype(np.int32)
+    n = rng.integers(0, 9, R)
+    cu = H.starts(n)
+    N_ = int(cu[-1])
+    held = np.where(rng.random(R) < 0.4, cur, cur + n).astype(np.int32)
+    par = np.concatenate([H.random_parents(rng, int(x)) for x in n]).astype(np.int32)
+    tok = rng.integers(0, V, N_).astype(np.int32)
+    logits = rng.normal(0, 1, (N_, V)).astype(np.float32)
+    for r in range(R):
+        for i in range(1, n[r]):
+            logits[cu[r] + par[cu[r] + i], tok[cu[r] + i]] = 9.0
+    want = O.verify_tree(logits, cu, tok, par, nodes, cur, held)
+    down = np.nonzero((n > 0) & (cur + n > held))[0]
+    assert len(down) > 5 and (want[0][down] == -1).all() and (want[0] > 0).sum() > 5
+    bad = logits.copy()
+    for r in down:                       # as the logits of NaN rows would be
+        bad[cu[r]:cu[r + 1]] = np.nan
+    acc, path, nxt, top = D.dspark_verify_tree(dev(bad), dev(cu), dev(tok), dev(par), nodes, ctx_len=dev(cur), mapped_len=dev(held))
+    torch.cuda.synchronize()
+    assert np.array_equal(acc.cpu().numpy(), want[0]) and np.array_equal(path.cpu().numpy(), want[1])
+    assert np.array_equal(nxt.cpu().numpy(), want[2])
+    live = np.ones(N_, bool)
+    for r in down:
+        live[cu[r]:cu[r + 1]] = False
+    assert np.array_equal(top.cpu().numpy()[live], want[3][live])
+    with pytest.raises(ValueError):
+        D.dspark_verify_tree(dev(logits), dev(cu), dev(tok), dev(par), nodes, mapped_len=dev(held))
+    with pytest.raises(ValueError):
+        D.dspark_verify_tree(dev(logits), dev(cu), dev(tok), dev(par), nodes, ctx_len=dev(cur[1:]), mapped_len=dev(held))
+
+
+@pytest.mark.parametrize("pages", [5, 8, 11])
+def test_steps_over_a_short_pool(pages):
+    # Whole steps with fewer pages than the batch would like, requests that end and begin
+    # again, and rows of the table that name pages of others: every request's cache holds what
+    # it accepted, every length is right, and no page is held twice or lost.
+    print(f"case short pool steps pages={pages}", flush=True)
+    rng = np.random.default_rng(pages)
+    R, Hk, Dh, V, width, nodes = 7, 1, 64, 50, 6, 12
+    kc = torch.full((pages, Hk, Dh // 8, P, 8), -1.0, dtype=torch.bfloat16, device=DEV)
+    vc = torch.full((pages, Hk, Dh, P), -1.0, dtype=torch.bfloat16, device=DEV)
+    table = dev(rng.integers(0, pages, (R, width)).astype(np.int32))        # stale ids from the start
+    ring, pool = dev(rng.permutation(pages).astype(np.int32)), dev(np.array([0, pages, 0, 0], np.int32))
+    lens = dev(np.zeros(R, np.int32))
+    held = [[] for _ in range(R)]            # the element numbers that each request's cache should hold
+    serial = turned_down = moved = 0
+    for step in range(25):
+        n = rng.integers(0, 20, R) if step == 0 else rng.integers(0, nodes + 1, R)
+        n = np.where([len(h) + x > width * P for h, x in zip(held, n)], 1, n)
+        cu = H.starts(n)
+        N_ = int(cu[-1])
+        par = np.concatenate([H.random_parents(rng, int(x)) for x in n] + [np.zeros(0)]).astype(np.int32)
+        tok = rng.integers(0, V, N_).astype(np.int32)
+        ids = serial + np.arange(N_)
+        serial += N_
+        rows = np.zeros((N_, Hk, Dh), np.float32)
+        rows[..., 0::2], rows[..., 1::2] = (ids // 128)[:, None, None], (ids % 128)[:, None, None]    # exact in bf16
+        kv = torch.from_numpy(rows).to(torch.bfloat16).to(DEV)
+        logits = rng.normal(0, 1, (N_, V)).astype(np.float32)
+        for r in range(R):
+            for i in range(1, n[r]):
+                if rng.random() < 0.7:
+                    logits[cu[r] + par[cu[r] + i], tok[cu[r] + i]] = 9.0
+        dcu, dpar, dtok = dev(cu), dev(par), dev(tok)
+        slots, new, pool1 = D.dspark_page_map(lens, dcu, table, ring, pool, P, N_)
+        mask, _ = D.dspark_tree_pack(dpar, dcu, 1, lens)
+        D.dspark_kv_store(kv, kv, slots, kc, vc, count=dcu[R:])
+        out, _ = D.dspark_tree_attention(kv, kc, vc, table, lens, dcu, tree_mask=mask, mapped_len=new)
+        z = dev(logits) + out[:, 0, :1].float() * 0.0        # NaN where the rows are
+        acc, path, nxt, _ = D.dspark_verify_tree(z, dcu, dtok, dpar, 20, ctx_len=lens, mapped_len=new)
+        kept = D.dspark_kv_commit(kc, vc, table, lens, path, acc, mapped_len=new)
+        end = rng.random(R) < 0.08
+        keep = torch.where(dev(end), torch.zeros_like(kept), kept)
+        pool = D.dspark_page_trim(new, keep, table, ring, pool1, P)
+        torch.cuda.synchronize()
+        a, p, was, now = (x.cpu().numpy() for x in (acc, path, lens, new))
+        assert int(pool[2]) == 0
+        for r in range(R):
+            down = n[r] > 0 and now[r] == was[r]
+            turned_down += int(down)
+            rows_ = out[int(cu[r]):int(cu[r + 1])]
+            assert torch.isnan(rows_).all() if down else torch.isfinite(rows_).all()
+            assert (a[r] == -1) == (down or n[r] == 0) and (int(nxt[r]) == -1) == (a[r] == -1)
+            held[r] += [int(ids[cu[r] + p[r, i]]) for i in range(a[r] + 1)]
+            moved += int(a[r] >= 0 and (p[r, :a[r] + 1] != np.arange(a[r] + 1)).any())
+            assert int(kept[r]) == len(held[r])
+            if end[r]:
+                held[r] = []
+        lens = keep
+        t, k, v = table.cpu().numpy(), H.np64(kc), H.np64(vc)
+        used = []
+        for r in range(R):
+            pos = np.arange(len(held[r]))
+            page, o = t[r, pos // P], pos % P
+            for lo, hi in ((k[page, 0, 0, o, 0], k[page, 0, 0, o, 1]), (v[page, 0, 0, o], v[page, 0, 1, o]),
+                           (k[page, 0, 7, o, 6], k[page, 0, 7, o, 7]), (v[page, 0, 62, o], v[page, 0, 63, o])):
+                assert (lo * 128 + hi).astype(int).tolist() == held[r], (step, r)
+            used += t[r, :-(-len(held[r]) // P)].tolist()
+        head, count, _, _ = pool.tolist()
+        free = [int(ring[(head + i) % pages]) for i in range(count)]
+        assert sorted(used + free) == list(range(pages)), step
+    print(f"  turned down {turned_down}, moved {moved}", flush=True)
+    assert turned_down >= 5 and moved >= 10

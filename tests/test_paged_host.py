@@ -303,6 +303,17 @@ def test_tree_attention_ex_rejects(kw, want):
     assert D.lib().dspark_last_error() != b""
 
 
+@no_gpu
+@pytest.mark.parametrize("kw,want", [
+    (dict(z=None), EINVAL), (dict(R=0), EINVAL), (dict(V=0), EINVAL), (dict(ctx=None), EINVAL), (dict(mapped=None), EINVAL),
+])
+def test_verify_tree_ex_rejects(kw, want):
+    a = dict(z=P, ctx=P, mapped=P, R=2, V=100)
+    a.update(kw)
+    assert D.lib().dspark_verify_tree_ex(a["z"], P, P, P, a["ctx"], a["mapped"], a["R"], 8, 4, a["V"], P, P, P, P, None) == want
+    assert D.lib().dspark_last_error() != b""
+
+
 # ---- refusals of the binding: nothing that is not on a device is taken ----
 
 def test_binding_refuses_host_tensors():
