@@ -208,9 +208,11 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0f70);
   asm volatile("" ::: "memory");
 }
-// A barrier that waits for nothing else.
+// A barrier that waits for nothing but this wave's reads of LDS: what they read may be
+// overwritten behind it.
 __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
