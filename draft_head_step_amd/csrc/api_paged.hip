@@ -16,6 +16,20 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return a < b + m && b < a + n;
 }
 
+// Whether one of the n rows of `row` bytes at p, p + p_step, ... has a byte in common with
+// one of those at q, q + q_step, ...; at steps that differ, whether the ranges have.
+bool rows_meet(const void* p, int64_t p_step, const void* q, int64_t q_step, int64_t n,
+               int64_t row) {
+  if (!overlap(p, (size_t)((n - 1) * p_step + row), q, (size_t)((n - 1) * q_step + row)))
+    return false;
+  if (n == 1 || p_step != q_step) return true;
+  // row i of q begins m bytes behind the beginning of row i + k of p
+  const int64_t by = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p));
+  const int64_t k = by / p_step - (by % p_step < 0 ? 1 : 0);
+  const int64_t m = by - k * p_step;
+  return (m < row && -n < k && k < n) || (m + row > p_step && -n < k + 1 && k + 1 < n);
+}
+
 bool head_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 dspark_status check_pages(const char* who, int page_size, int max_pages, int num_pages) {
@@ -214,6 +228,10 @@ dspark_status dspark_tree_attention_ex(const void* q, int64_t q_stride, int dtyp
       out_stride < row)
     return fail(DSPARK_EINVAL, "tree_attention: rows and caches must be 16-byte aligned, rows at "
                                "least Hq * D apart");
+  // a row may be written where it was read, but nowhere that another is
+  if (!(out == q && (out_stride == q_stride || max_tokens == 1)) &&
+      dspark::rows_meet(q, q_stride * 2, out, out_stride * 2, max_tokens, row * 2))
+    return fail(DSPARK_EINVAL, "tree_attention: out may be q or apart from it, not a part of it");
   if (!dspark::head_dim_ok(D))
     return fail(DSPARK_EUNSUPPORTED, "tree_attention: D must be 64, 96, 128, 192 or 256 (got %d)", D);
   if (mask_words > DSPARK_MAX_MASK_WORDS)

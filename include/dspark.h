@@ -654,7 +654,7 @@ size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, in
  *   k_scale, v_scale  [Hk] fp32 with a DSPARK_E4M3 cache, NULL otherwise.
  *   scale       finite, also times log2(e).
  *   out         rows of [Hq, D] elements of `dtype`, row e at out + e * out_stride;
- *               may be q itself, with its stride.
+ *               may be q itself, with its stride, and no other part of its rows.
  *   lse         optional [max_tokens, Hq] fp32.
  *   workspace   >= dspark_tree_attention_workspace(...) bytes, 256-byte aligned;
  *               its contents on entry do not matter, and calls that may run at
@@ -667,8 +667,8 @@ size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, in
  * to the rounding of fp32 sums.
  * Errors: EINVAL for NULL pointers, sizes <= 0, Hq not a multiple of Hk, bad
  * types, page sizes, strides, alignment or scale, scales missing or given
- * without DSPARK_E4M3; EUNSUPPORTED for D outside {64, 96, 128, 192, 256},
- * mask_words > DSPARK_MAX_MASK_WORDS, R > 2^20 or max_tokens * Hq above 2^31 - 1;
+ * without DSPARK_E4M3, out on a part of q; EUNSUPPORTED for D outside
+ * {64, 96, 128, 192, 256}, mask_words > DSPARK_MAX_MASK_WORDS, R > 2^20 or max_tokens * Hq above 2^31 - 1;
  * EWORKSPACE; EDEVICE.
  */
 dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,

@@ -492,3 +492,22 @@ def test_seeded_sweep():
         out, lse = call(c, want_lse=True)
         torch.cuda.synchronize()
         check(c, out, lse)
+
+
+def test_outputs_on_parts_of_the_queries_are_refused():
+    print("case attention outputs on queries", flush=True)
+    c = make(70, [3, 2], [20, 5], 4, 2, 64, 16)
+    wide = torch.zeros((7, 12, 64), dtype=torch.bfloat16, device=DEV)
+    c["q"] = wide[:5, :4]
+    c["q"].copy_(make(70, [3, 2], [20, 5], 4, 2, 64, 16)["q"])
+    want = call(dict(c, q=c["q"].contiguous()))[0]
+    for out in (wide[1:6, :4], wide[:5, 1:5], wide[2:7, :4]):
+        with pytest.raises(D.DsparkError) as e:
+            call(c, out=out)
+        assert e.value.status == 1
+    got = call(c, out=wide[:5, 4:8])[0]              # beside them
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    call(c, out=c["q"])                              # on them
+    torch.cuda.synchronize()
+    assert torch.equal(c["q"], want)

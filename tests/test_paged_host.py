@@ -304,6 +304,32 @@ def test_tree_attention_ex_rejects(kw, want):
 
 
 @no_gpu
+@pytest.mark.parametrize("q,qs,out,os_,n,meet", [
+    # rows of 512 elements, offsets in elements; EWORKSPACE is the next refusal
+    (0, 512, 0, 512, 4, False), (0, 1024, 0, 1024, 4, False), (0, 512, 0, 1024, 1, False),       # q itself
+    (0, 512, 0, 1024, 4, True), (0, 1024, 0, 512, 2, True),                                       # with another stride
+    (0, 512, 512, 512, 4, True), (512, 512, 0, 512, 4, True), (0, 512, 8, 512, 1, True), (8, 512, 0, 512, 1, True),
+    (0, 512, 2048, 512, 4, False), (2048, 512, 0, 512, 4, False), (0, 512, 2040, 512, 4, True), (0, 512, 512, 512, 1, False),
+    (0, 1024, 512, 1024, 4, False), (512, 1024, 0, 1024, 4, False),                               # side by side in wider rows
+    (0, 1536, 512, 1536, 4, False), (0, 1536, 1024, 1536, 4, False), (0, 1024, 504, 1024, 4, True), (0, 1024, 520, 1024, 4, True),
+    (0, 1024, 520, 1024, 1, False), (520, 1024, 0, 1024, 4, True), (504, 1024, 0, 1024, 4, True),
+    (0, 1024, 4 * 1024 - 8, 1024, 4, False), (0, 1024, 3 * 1024 + 504, 1024, 4, True), (0, 1024, 3 * 1024 + 512, 1024, 4, False),
+    (0, 1024, 3 * 1024, 1024, 4, True), (0, 1024, -3 * 1024, 1024, 4, True), (0, 1024, -4 * 1024 + 520, 1024, 4, True),
+    (0, 1024, -4 * 1024 + 512, 1024, 4, False), (0, 512, 4096, 1024, 4, False),
+])
+def test_tree_attention_refuses_outputs_on_parts_of_the_queries(q, qs, out, os_, n, meet):
+    base = 16 * P
+    st = D.lib().dspark_tree_attention(base + 2 * q, qs, 0, P, P, 0, None, None, P, P, P, None, 0, 2, n, 8, 2, 64, 16, 4, 9, 0.125,
+                                       base + 2 * out, os_, None, None, 0, None)
+    assert st == (EINVAL if meet else EWORKSPACE)
+    # the definition: byte by byte over the rows
+    if not (q == out and (qs == os_ or n == 1)) and qs == os_:
+        a = set(x for i in range(n) for x in range(q + i * qs, q + i * qs + 512, 8))
+        b = set(x for i in range(n) for x in range(out + i * os_, out + i * os_ + 512, 8))
+        assert meet == bool(a & b)
+
+
+@no_gpu
 @pytest.mark.parametrize("kw,want", [
     (dict(z=None), EINVAL), (dict(R=0), EINVAL), (dict(V=0), EINVAL), (dict(ctx=None), EINVAL), (dict(mapped=None), EINVAL),
 ])
