@@ -51,11 +51,25 @@ _LIB = None
 def __getattr__(name):
     # paged.py needs PyTorch at import; the package itself does not
     if name in _PAGED:
-        from . import paged
+        try:
+            from . import paged
+        except ModuleNotFoundError as e:
+            if e.name != "torch":
+                raise
+            return _until_called(name)
         for n in _PAGED:
             globals()[n] = getattr(paged, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def _until_called(name):
+    """A name of paged.py without PyTorch: it can be had, and a call raises."""
+    def entry(*args, **kwargs):
+        from . import paged
+        return getattr(paged, name)(*args, **kwargs)
+    entry.__name__ = entry.__qualname__ = name
+    return entry
 
 
 def lib_path() -> str:

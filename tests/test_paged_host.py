@@ -5,6 +5,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -354,6 +355,21 @@ def test_binding_refuses_host_tensors():
               lambda: D.dspark_tree_pack(i, cu, 1), lambda: D.dspark_verify_tree(torch.zeros((4, 9)), cu, i, i, 4)):
         with pytest.raises(ValueError, match="device"):
             f()
+
+
+def test_every_name_of_the_package_can_be_had_without_pytorch():
+    code = ("import sys\n"
+            "sys.modules['torch'] = None\n"
+            "from draft_head_step_amd import *\n"
+            "import draft_head_step_amd as D\n"
+            "assert all(hasattr(D, n) for n in D.__all__)\n"
+            "assert dspark_page_map.__name__ == 'dspark_page_map'\n"
+            "try:\n"
+            "    dspark_page_map()\n"
+            "except ImportError:\n"
+            "    print('raised')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "raised", r.stderr
 
 
 # ---- pins of the oracle ----
