@@ -587,7 +587,8 @@ dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, in
  * new_len[r] = ctx_len[r] + 1 + accepted[r].  accepted[r] = -1 (a request
  * without elements) moves nothing and gives new_len[r] = ctx_len[r].
  *   k_cache, v_cache  caches of `layers` layers, layer l at l * k_layer_stride
- *               (v_layer_stride) elements (multiples of 16 / element size).
+ *               (v_layer_stride) elements (multiples of 16 / element size; a
+ *               layer apart at least).
  *   path        [R, max_nodes] int32: 0, then strictly increasing node numbers (as
  *               dspark_verify_tree writes them).
  * A request whose path is not such a sequence, whose accepted count lies
@@ -597,8 +598,8 @@ dspark_status dspark_kv_store(const void* k, const void* v, int64_t k_stride, in
  * Behind the pages that a request holds its block_table row may name pages of
  * others: where a pool can run short, dspark_kv_commit_ex is the call to use.
  * Errors: EINVAL for NULL pointers, sizes <= 0, a bad page size or type,
- * misaligned caches or strides, new_len on ctx_len or accepted; EUNSUPPORTED
- * for D as above, layers > 65535 or R > 65535; EDEVICE.
+ * misaligned caches or strides, layers that overlap, new_len on ctx_len or
+ * accepted; EUNSUPPORTED for D as above, layers > 65535 or R > 65535; EDEVICE.
  */
 dspark_status dspark_kv_commit(void* k_cache, void* v_cache, int64_t k_layer_stride,
                                int64_t v_layer_stride, int layers, int cache_dtype,

@@ -291,6 +291,17 @@ def test_kv_commit_ex_rejects(kw, want):
 
 
 @no_gpu
+@pytest.mark.parametrize("kl,vl,layers,want", [
+    # a layer is 9 * 2 * 64 * 16 = 18432 elements; new_len on ctx_len is the next refusal either way
+    (0, 18432, 2, b"overlap"), (18432, 0, 2, b"overlap"), (18424, 18432, 3, b"overlap"), (-18424, 18432, 3, b"overlap"),
+    (8, 8, 2, b"overlap"), (18432, 18432, 3, b"new_len"), (-18432, 18440, 3, b"new_len"), (0, 0, 1, b"new_len"),
+])
+def test_kv_commit_refuses_layers_on_each_other(kl, vl, layers, want):
+    assert D.lib().dspark_kv_commit(P, P, kl, vl, layers, 0, P, P, P, P, 2, 8, 2, 64, 16, 4, 9, P, None) == EINVAL
+    assert want in D.lib().dspark_last_error()
+
+
+@no_gpu
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(R=0), EINVAL), (dict(Hq=9), EINVAL), (dict(D=48, qs=512), EUNSUPPORTED),
     (dict(scale=float("nan")), EINVAL), (dict(ws=None), EWORKSPACE),
