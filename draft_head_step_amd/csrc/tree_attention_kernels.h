@@ -243,7 +243,7 @@ struct Req {
   int n;            // elements that are visible to each other
   int rows;         // query rows to compute (elements within max_tokens, times heads a group)
   int ctx, total;   // positions before the segment, and with it
-  int full;         // row tiles with four waves over rows
+  int full;         // row tiles with all waves over rows
   int wr_last;      // waves over rows of the last one, 0 if there is none
   int units_full, units_last;   // units of a tile
   bool bad;
@@ -1096,9 +1096,11 @@ dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
 }
 template <int DT, bool F8, int D>
 dspark_status go(const TreeAttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  return p.ring      ? go<DT, F8, D, 2, true>(a, p, stream)
-         : p.nt == 1 ? go<DT, F8, D, 1, false>(a, p, stream)
-                     : go<DT, F8, D, 2, false>(a, p, stream);
+  if (p.ring) return go<DT, F8, D, 2, true>(a, p, stream);
+  // (heads above 128 share a ring from two tiles on)
+  if constexpr (D <= 128)
+    if (p.nt == 2) return go<DT, F8, D, 2, false>(a, p, stream);
+  return go<DT, F8, D, 1, false>(a, p, stream);
 }
 
 }  // namespace
