@@ -279,3 +279,58 @@ def test_allocations_of_a_call_belong_to_its_stream():
     out = D.dspark_tree_attention(s["q"], s["kc"], s["vc"], s["table"], zero, s["cu"], stream=side)[0]
     side.synchronize()
     assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+
+
+class _Spy:
+    """The library, with the arguments of every call kept."""
+
+    def __init__(self, lib):
+        self.lib, self.calls = lib, []
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return f(*args)
+        return call
+
+
+def _stream_of(address):
+    """The stream that the allocator's block at an address belongs to."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= address < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("no block at that address")
+
+
+def test_memory_of_a_call_is_the_streams_own(monkeypatch):
+    # A workspace is released when the call returns: only a block of the call's own stream is
+    # safe from other streams' work then.  Outputs that the binding makes are such blocks too.
+    print("case paged stream ownership", flush=True)
+    s = _step_state(11)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    spy = _Spy(D.lib())
+    monkeypatch.setattr(D, "_LIB", spy)
+    for stream in (side, None):
+        want = side.cuda_stream if stream is side else torch.cuda.current_stream().cuda_stream
+        spy.calls.clear()
+        made = []
+        slots, new, pool = D.dspark_page_map(s["ctx"], s["cu"], s["table"], s["ring"], s["pool"], P, s["N"], stream=stream)
+        made += [slots, new, pool]
+        made += D.dspark_tree_pack(s["par"], s["cu"], 1, s["ctx"], want_req=True, stream=stream)
+        made += D.dspark_tree_attention(s["q"], s["kc"], s["vc"], s["table"], s["ctx"], s["cu"], tree_mask=made[3], mapped_len=new,
+                                        want_lse=True, stream=stream)
+        acc, path, nxt, top = D.dspark_verify_tree(s["logits"], s["cu"], s["tok"], s["par"], s["n"], ctx_len=s["ctx"], mapped_len=new,
+                                                   stream=stream)
+        made += [acc, path, nxt, top]
+        kc, vc = s["kc"].clone(), s["vc"].clone()
+        torch.cuda.synchronize()
+        kept = D.dspark_kv_commit(kc, vc, s["table"], s["ctx"], path, acc, mapped_len=new, stream=stream)
+        made += [kept, D.dspark_page_trim(new, s["ctx"], s["table"], s["ring"].clone(), pool, P, stream=stream)]
+        torch.cuda.synchronize()
+        assert [_stream_of(t.data_ptr()) for t in made] == [want] * 14
+        (ws,) = [a[-3] for n, a in spy.calls if n == "dspark_tree_attention_ex"]
+        assert _stream_of(ws) == want
+        assert all(a[-1] == want for n, a in spy.calls if n != "dspark_tree_attention_workspace")

@@ -511,3 +511,14 @@ def test_outputs_on_parts_of_the_queries_are_refused():
     call(c, out=c["q"])                              # on them
     torch.cuda.synchronize()
     assert torch.equal(c["q"], want)
+
+
+@pytest.mark.parametrize("width", [40, 5000, 70000])
+@pytest.mark.parametrize("n,ctx,tree", [([1], [200], False), ([6, 0, 2], [200, 31, 500], False), ([40, 9], [90, 300], True)])
+def test_tables_much_wider_than_the_requests(n, ctx, tree, width):
+    # what a server's table looks like; ids behind a request's last page are no one's
+    print(f"case attention width {width} n={n} ctx={ctx}", flush=True)
+    c = make(71, n, ctx, 8, 2, 128, 16, tree=tree, width=width)
+    out, lse = call(c, want_lse=True)
+    torch.cuda.synchronize()
+    check(c, out, lse)
