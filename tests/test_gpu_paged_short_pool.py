@@ -268,3 +268,74 @@ def test_steps_over_a_short_pool(pages):
         assert sorted(used + free) == list(range(pages)), step
     print(f"  turned down {turned_down}, moved {moved}", flush=True)
     assert turned_down >= 5 and moved >= 10
+
+
+def test_a_step_over_a_short_pool_replays_in_a_graph():
+    # the whole step with its commit; what it changes in place is put back between the replays
+    print("case short pool graph", flush=True)
+    rng = np.random.default_rng(8)
+    R, pages, Hk, Dh, V, nodes = 6, 30, 2, 64, 40, 9
+    cur = rng.integers(0, 60, R).astype(np.int32)
+    n = rng.integers(3, nodes + 1, R)
+    cu = H.starts(n)
+    N_ = int(cu[-1])
+    need = -(-cur // P)
+    table = np.resize(rng.permutation(pages), (R, 5)).astype(np.int32)      # every row full of ids
+    order = rng.permutation(pages).astype(np.int32)
+    at = 0
+    for r in range(R):
+        table[r, :need[r]] = order[at:at + need[r]]
+        at += need[r]
+    ring = np.full(pages, -1, np.int32)
+    ring[:2] = order[at:at + 2]                                            # two pages for all of them
+    par = np.concatenate([H.random_parents(rng, int(x)) for x in n]).astype(np.int32)
+    tok = rng.integers(0, V, N_).astype(np.int32)
+    logits = rng.normal(0, 1, (N_, V)).astype(np.float32)
+    for r in range(R):
+        for i in range(1, n[r]):
+            logits[cu[r] + par[cu[r] + i], tok[cu[r] + i]] = 9.0
+    kc, vc = H.caches(rng, pages, Hk, Dh, P, "bf16", DEV)
+    start = dict(table=dev(table), ring=dev(ring), kc=kc, vc=vc)
+    s = {k: t.clone() for k, t in start.items()}
+    c, u, p, t, z = dev(cur), dev(cu), dev(par), dev(tok), dev(logits)
+    pool = dev(np.array([0, 2, 0, 0], np.int32))
+    x = torch.from_numpy(rng.normal(0, 1, (N_, Hk, Dh)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    o = dict(slots=torch.zeros(N_, dtype=torch.int64, device=DEV), new=torch.zeros(R, **i32), a=torch.zeros(4, **i32),
+             b=torch.zeros(4, **i32), mask=torch.zeros(N_, 1, **i32), out=torch.zeros_like(x), acc=torch.zeros(R, **i32),
+             path=torch.zeros(R, nodes, **i32), nxt=torch.zeros(R, **i32), top=torch.zeros(N_, **i32), kept=torch.zeros(R, **i32),
+             ws=torch.zeros(D.dspark_tree_attention_workspace(R, N_, Hk, Hk, Dh), dtype=torch.uint8, device=DEV))
+
+    def step():
+        D.dspark_page_map(c, u, s["table"], s["ring"], pool, P, slots=o["slots"], new_len=o["new"], pool_out=o["a"])
+        D.dspark_tree_pack(p, u, 1, c, mask=o["mask"])
+        D.dspark_kv_store(x, x, o["slots"], s["kc"], s["vc"], count=u[R:])
+        D.dspark_tree_attention(x, s["kc"], s["vc"], s["table"], c, u, tree_mask=o["mask"], mapped_len=o["new"], out=o["out"],
+                                workspace=o["ws"])
+        D.dspark_verify_tree(z, u, t, p, nodes, ctx_len=c, mapped_len=o["new"], target_argmax=o["top"], accepted=o["acc"],
+                             path=o["path"], next_token=o["nxt"])
+        D.dspark_kv_commit(s["kc"], s["vc"], s["table"], c, o["path"], o["acc"], mapped_len=o["new"], new_len=o["kept"])
+        D.dspark_page_trim(o["new"], o["kept"], s["table"], s["ring"], o["a"], P, pool_out=o["b"])
+
+    step()
+    torch.cuda.synchronize()
+    down = (o["new"].cpu().numpy() == cur)
+    assert 0 < down.sum() < R and (o["kept"].cpu().numpy()[down] == cur[down]).all() and (o["acc"].cpu().numpy()[~down] > 0).all()
+    want = {k: v.clone() for k, v in {**s, **o}.items() if k != "ws"}
+    for k, v in start.items():
+        s[k].copy_(v)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rep in range(3):
+        for k, v in start.items():
+            s[k].copy_(v)
+        for v in o.values():
+            v.view(torch.uint8).fill_(0xA5 + rep)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in want.items():
+            got = s[k] if k in s else o[k]
+            assert torch.equal(got.view(torch.uint8), v.view(torch.uint8)), (rep, k)
