@@ -16,11 +16,14 @@
 //              for i = 1, 2, ... in turn, four positions' loads at a time.
 //              path[i] >= i and path increases, so position i, once written, is
 //              no later source.  Places in the cache are worked out once per
-//              request, in LDS.  A value channel's positions are neighbours, so a
-//              moved byte touches a whole 64-byte piece of memory on both sides:
-//              that, not the bytes moved, is what the call costs: 64 paths in 32
-//              layers of 8 heads of 128 in e4m3 (20 MB to read and write) take
-//              46 to 56 us, one layer of 32 paths in bf16 6.9.
+//              request, in LDS.  Values move one number at a time, and 64 lanes
+//              of a load or store touch 64 channels, each a page's width from the
+//              next: 64 paths in 32 layers of 8 heads of 128 in e4m3 (20 MB to
+//              read and write) take 35 us in pages of 16, 58 in pages of 32 and 140
+//              in pages of 128 (bf16: 83, 124 and 162).  In pages of 32 the counters
+//              see 52 MB read and 78 written, half of what a copy moves in that
+//              time, so the accesses and not the bytes are what it costs.  One
+//              layer of 32 paths in bf16 takes 6.9.
 #include <type_traits>
 
 #include "dspark_internal.h"

@@ -37,8 +37,15 @@ AttnPlan plan_tree_attention(int R, int max_tokens, int Hq, int Hk, int D, int64
   const int waves = attn_group(D, p.ring);
   const int per_cu = attn_waves(p.nt, D, p.ring) * 4 / waves;   // four SIMDs
   int64_t groups = (int64_t)compute_units() * per_cu;
-  // Up to 512 positions a tile is at most four steps of every wave: cutting it would
-  // cost more than it spreads.
+  // A tile of up to 512 positions is not cut, and the second launch is left out.  Whole
+  // and cut, in us, tables of 512 positions, 32 heads over 8 of 128:
+  //   requests x elements   1 x 6  8 x 6  64 x 6  256 x 6  1 x 64  1 x 300  8 x 64  64 x 64
+  //   whole                  12.2   14.5    32.3    110.2    32.9     39.9    34.8     72.4
+  //   cut                    15.0   20.7    35.0    112.6    29.9     30.2    33.8     74.9
+  // (four waves over positions take 512 in four steps each; where all waves are over rows
+  // they take 16, and one request of many rows loses: 1 x 64 over 164 positions 20.9 and
+  // 24.9 again).  The rule goes by the table's width, all that the host knows: one token
+  // over 200 positions takes 11.9 us with a table of 512 positions, 14.9 with a wider one.
   p.whole = capacity > 0 && capacity <= 512;
   if (capacity > 0) {
     // no more workgroups than units of work there can be

@@ -544,7 +544,11 @@ dspark_status dspark_page_map(const int32_t* cur_len, const int32_t* cu_seqlens,
  * give_r = ceil(cur_len[r] / P) - ceil(keep_len[r] / P) and S its running sum,
  *     ring[(head + count + S_r + i) mod num_pages] = block_table[r, ceil(keep_len[r] / P) + i]
  * and the pool's count grows by the sum.  block_table is not changed: the
- * entries behind the last kept page are simply not read any more.
+ * entries behind the last kept page are not read by page calls any more (other
+ * calls learn from mapped_len where a request ends).  Page ids go back as the
+ * row names them.  A keep_len of -1, as dspark_kv_commit gives it for a path
+ * that it refuses, is 0 and ends the request; with dspark_kv_commit_ex the
+ * request keeps its context.
  * A request with cur_len[r] < 0 or more than max_pages pages gives nothing and
  * counts in pool_out->refused; if the ring would hold more than num_pages
  * pages (pages given back twice) nothing is written to it and refused = R.
