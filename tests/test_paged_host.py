@@ -318,16 +318,16 @@ def test_tree_attention_ex_rejects(kw, want):
 @no_gpu
 @pytest.mark.parametrize("q,qs,out,os_,n,meet", [
     # rows of 512 elements, offsets in elements; EWORKSPACE is the next refusal
-    (0, 512, 0, 512, 4, False), (0, 1024, 0, 1024, 4, False), (0, 512, 0, 1024, 1, False),       # q itself
-    (0, 512, 0, 1024, 4, True), (0, 1024, 0, 512, 2, True),                                       # with another stride
+    (0, 512, 0, 512, 4, False), (0, 1040, 0, 1040, 4, False), (0, 512, 0, 1040, 1, False),       # q itself
+    (0, 512, 0, 1040, 4, True), (0, 1040, 0, 512, 2, True),                                       # with another stride
     (0, 512, 512, 512, 4, True), (512, 512, 0, 512, 4, True), (0, 512, 8, 512, 1, True), (8, 512, 0, 512, 1, True),
     (0, 512, 2048, 512, 4, False), (2048, 512, 0, 512, 4, False), (0, 512, 2040, 512, 4, True), (0, 512, 512, 512, 1, False),
-    (0, 1024, 512, 1024, 4, False), (512, 1024, 0, 1024, 4, False),                               # side by side in wider rows
-    (0, 1536, 512, 1536, 4, False), (0, 1536, 1024, 1536, 4, False), (0, 1024, 504, 1024, 4, True), (0, 1024, 520, 1024, 4, True),
-    (0, 1024, 520, 1024, 1, False), (520, 1024, 0, 1024, 4, True), (504, 1024, 0, 1024, 4, True),
-    (0, 1024, 4 * 1024 - 8, 1024, 4, False), (0, 1024, 3 * 1024 + 504, 1024, 4, True), (0, 1024, 3 * 1024 + 512, 1024, 4, False),
-    (0, 1024, 3 * 1024, 1024, 4, True), (0, 1024, -3 * 1024, 1024, 4, True), (0, 1024, -4 * 1024 + 520, 1024, 4, True),
-    (0, 1024, -4 * 1024 + 512, 1024, 4, False), (0, 512, 4096, 1024, 4, False),
+    (0, 1040, 512, 1040, 4, False), (512, 1040, 0, 1040, 4, False),                               # side by side in wider rows
+    (0, 1536, 512, 1536, 4, False), (0, 1536, 1024, 1536, 4, False), (0, 1040, 504, 1040, 4, True), (0, 1040, 536, 1040, 4, True),
+    (0, 1040, 536, 1040, 1, False), (536, 1040, 0, 1040, 4, True), (504, 1040, 0, 1040, 4, True),
+    (0, 1040, 4 * 1040 - 8, 1040, 4, False), (0, 1040, 3 * 1040 + 504, 1040, 4, True), (0, 1040, 3 * 1040 + 512, 1040, 4, False),
+    (0, 1040, 3 * 1040, 1040, 4, True), (0, 1040, -3 * 1040, 1040, 4, True), (0, 1040, -4 * 1040 + 536, 1040, 4, True),
+    (0, 1040, -4 * 1040 + 512, 1040, 4, False), (0, 512, 4096, 1040, 4, False),
 ])
 def test_tree_attention_refuses_outputs_on_parts_of_the_queries(q, qs, out, os_, n, meet):
     base = 16 * P
