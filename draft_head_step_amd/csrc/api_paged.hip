@@ -165,8 +165,8 @@ dspark_status dspark_kv_commit_ex(void* k_cache, void* v_cache, int64_t k_layer_
     return fail(DSPARK_EINVAL, "kv_commit: caches and layers must be 16-byte aligned");
   // a layer's workgroups wait for no other layer's
   const __int128 layer = (__int128)num_pages * page_size * Hk * D;
-  if (layers > 1 && ((k_layer_stride < layer && -k_layer_stride < layer) ||
-                     (v_layer_stride < layer && -v_layer_stride < layer)))
+  const __int128 kl = k_layer_stride, vl = v_layer_stride;
+  if (layers > 1 && ((kl < layer && -kl < layer) || (vl < layer && -vl < layer)))
     return fail(DSPARK_EINVAL, "kv_commit: the layers of a cache overlap");
   // every layer's workgroups read the lengths, one of them writes the new ones
   const size_t lens = (size_t)R * sizeof(int32_t);

@@ -316,8 +316,9 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_seqlens,
             q.data_ptr(), qs, _CACHE[q.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
             _CACHE[k_cache.dtype], sk, sv, block_table.data_ptr(), ctx_len.data_ptr(),
             0 if mapped_len is None else mapped_len.data_ptr(), cu_seqlens.data_ptr(),
-            0 if tree_mask is None else tree_mask.data_ptr(), words, R, N, hq, hk, d, p, mp, n, 1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
-            os_, 0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            0 if tree_mask is None else tree_mask.data_ptr(), words, R, N, hq, hk, d, p, mp, n,
+            1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(), os_,
+            0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), s)
     if st:
         _D._check(st, "dspark_tree_attention")
@@ -395,8 +396,8 @@ def dspark_verify_tree(target_logits, cu_seqlens, tokens, parents, max_nodes, *,
         st = (_D._LIB or _D.lib()).dspark_verify_tree_ex(
             target_logits.data_ptr(), cu_seqlens.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
             0 if mapped_len is None else ctx_len.data_ptr(),
-            0 if mapped_len is None else mapped_len.data_ptr(), R, N, max_nodes, V, target_argmax.data_ptr(), accepted.data_ptr(), path.data_ptr(),
-            next_token.data_ptr(), s)
+            0 if mapped_len is None else mapped_len.data_ptr(), R, N, max_nodes, V,
+            target_argmax.data_ptr(), accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), s)
     if st:
         _D._check(st, "dspark_verify_tree")
     return accepted, path, next_token, target_argmax

@@ -513,8 +513,7 @@ typedef struct {
  * slots[cu_seqlens[r] + j] is the slot of position cur_len[r] + j and
  * new_len[r] = cur_len[r] + n_r.  A request that is not served (the pool is
  * short, cur_len[r] or n_r negative, more than max_pages pages or 2^31 - 1 tokens)
- * leaves its
- * block_table row as it was, gets slots of -1 and new_len[r] = cur_len[r], and
+ * leaves its block_table row as it was, gets slots of -1 and new_len[r] = cur_len[r], and
  * counts in pool_out->refused; one that asks for no page is served whatever
  * the pool holds, and one with too many pages takes none from the others.  A
  * slot whose page id lies outside [0, num_pages) is -1.
@@ -673,8 +672,8 @@ size_t dspark_tree_attention_workspace(int R, int max_tokens, int Hq, int Hk, in
  * Errors: EINVAL for NULL pointers, sizes <= 0, Hq not a multiple of Hk, bad
  * types, page sizes, strides, alignment or scale, scales missing or given
  * without DSPARK_E4M3, out on a part of q; EUNSUPPORTED for D outside
- * {64, 96, 128, 192, 256}, mask_words > DSPARK_MAX_MASK_WORDS, R > 2^20 or max_tokens * Hq above 2^31 - 1;
- * EWORKSPACE; EDEVICE.
+ * {64, 96, 128, 192, 256}, mask_words > DSPARK_MAX_MASK_WORDS, R > 2^20 or
+ * max_tokens * Hq above 2^31 - 1; EWORKSPACE; EDEVICE.
  */
 dspark_status dspark_tree_attention(const void* q, int64_t q_stride, int dtype,
                                     const void* k_cache, const void* v_cache, int cache_dtype,
